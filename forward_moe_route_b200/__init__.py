@@ -53,6 +53,13 @@ class MoePeerRows(ctypes.Structure):
                 ("n_ranks", ctypes.c_int32)]
 
 
+class MoeNormDesc(ctypes.Structure):
+    """moe_norm_desc: the norms around a layer."""
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("n_slots", ctypes.c_int32),
+                ("gate_group", ctypes.c_int32), ("act_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("res_scale", ctypes.c_float)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -61,6 +68,7 @@ class MoeError(RuntimeError):
 
 _P = ctypes.c_void_p
 _D = ctypes.POINTER(MoeLayerDesc)
+_ND = ctypes.POINTER(MoeNormDesc)
 _SIGS = {
     "moe_workspace_size": (ctypes.c_size_t, [_D]),
     "moe_route": (ctypes.c_int, [_D, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
@@ -116,6 +124,12 @@ _SIGS = {
                                         ctypes.c_size_t, _P]),
     "moe_backward_saved": (ctypes.c_int, [_D, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                           ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "moe_norm": (ctypes.c_int, [_ND, _P, _P, _P, _P]),
+    "moe_combine_norm": (ctypes.c_int, [_ND, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_norm_backward_workspace_size": (ctypes.c_size_t, [_ND]),
+    "moe_norm_backward": (ctypes.c_int, [_ND, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_combine_norm_backward": (ctypes.c_int, [_ND, _P, _P, _P, _P, _P, _P, _P, _P,
+                                                 ctypes.c_size_t, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -651,3 +665,127 @@ def moe_expert_ffn_fp8(desc, n_experts: int, groups, n_rows_in: int, n_rows_out:
                                    _ptr(group_out), _ptr(ws),
                                    ws.numel() if ws is not None else 0, _stream(stream)),
            "moe_expert_ffn_fp8")
+
+
+# ---- norms around the layer, grouped products and the optimiser step -------------------------
+
+def _operand(where: str, name: str, t, numel: int, dtypes, optional: bool = False) -> None:
+    """Refuse a tensor that is missing, strided, short or of another type.  Address arguments
+    (int) pass unchecked."""
+    if t is None:
+        if not optional:
+            raise MoeError(ERR_INVALID_ARG, f"{where}: {name} is missing")
+        return
+    if isinstance(t, int):
+        return
+    if not t.is_contiguous():
+        raise MoeError(ERR_INVALID_ARG, f"{where}: {name} is not contiguous")
+    kind = str(t.dtype).replace("torch.", "")
+    if kind not in dtypes:
+        raise MoeError(ERR_INVALID_ARG, f"{where}: {name} is {kind}, not {' or '.join(dtypes)}")
+    if t.numel() < numel:
+        raise MoeError(ERR_INVALID_ARG,
+                       f"{where}: {name} holds {t.numel()} elements, the call needs {numel}")
+
+
+def _on_device(where: str, tensors) -> None:
+    """Refuse (name, tensor) pairs that are not on the current device, whose stream the call
+    uses and whose memory its kernels address."""
+    import torch
+    for name, t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_cuda:
+            raise MoeError(ERR_INVALID_ARG, f"{where}: {name} is not a CUDA tensor")
+        if t.device.index != torch.cuda.current_device():
+            raise MoeError(ERR_INVALID_ARG,
+                           f"{where}: {name} is on {t.device}, the current device is "
+                           f"cuda:{torch.cuda.current_device()}")
+
+
+_ACT = {DT_F32: ("float32",), DT_BF16: ("bfloat16",)}
+
+
+def make_norm_desc(T: int, d: int, eps: float, dtype: str = "bf16", n_slots: int = 1,
+                   gate_group: int = 0, res_scale: float = 1.0) -> MoeNormDesc:
+    return MoeNormDesc(T, d, n_slots, gate_group, {"f32": DT_F32, "bf16": DT_BF16}[dtype], eps,
+                       res_scale)
+
+
+def moe_norm_backward_workspace_size(desc: MoeNormDesc) -> int:
+    return int(_lib.moe_norm_backward_workspace_size(ctypes.byref(desc)))
+
+
+def norm_backward_workspace(desc: MoeNormDesc, device="cuda"):
+    """A uint8 CUDA tensor of moe_norm_backward_workspace_size(desc) bytes."""
+    import torch
+    n = moe_norm_backward_workspace_size(desc)
+    if n == 0:
+        raise MoeError(ERR_INVALID_ARG, "moe_norm_backward_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _norm_operands(where: str, desc: MoeNormDesc, rows, vectors, dw=None, gates=(), slots=None,
+                   ws=None) -> None:
+    """rows: [T, d] tensors, vectors: [d], gates: [n_gate, d]; all (name, tensor, optional)."""
+    act = _ACT.get(desc.act_dtype)
+    if act is None:
+        raise MoeError(ERR_INVALID_ARG, f"{where}: act_dtype is not F32 or BF16")
+    T, d, g = desc.T, desc.d, desc.gate_group
+    n_gate = -(-T // g) if g > 0 else 0
+    for name, t, optional in rows:
+        _operand(where, name, t, T * d, act, optional)
+    for name, t, optional in vectors:
+        _operand(where, name, t, d, act, optional)
+    for name, t, optional in gates:
+        _operand(where, name, t, n_gate * d, act, optional)
+    if slots is not None:
+        _operand(where, "y_slots", slots, T * desc.n_slots * d, act)
+    if dw is not None:
+        _operand(where, "dw", dw, d, ("float32",))
+    if ws is not None:
+        _operand(where, "ws", ws, 0, ("uint8",))
+    _on_device(where, [r[:2] for r in (*rows, *vectors, *gates)] +
+               [("y_slots", slots), ("dw", dw), ("ws", ws)])
+
+
+def moe_norm(desc, x, w, out, stream=None) -> None:
+    """out = x * rsqrt(mean(x^2) + eps) * w, row by row."""
+    _norm_operands("moe_norm", desc, [("x", x, False), ("out", out, False)], [("w", w, False)])
+    _check(_lib.moe_norm(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(out), _stream(stream)),
+           "moe_norm")
+
+
+def moe_combine_norm(desc, x_residual, y_slots, w, gate, w_next, h, y, x_next,
+                     stream=None) -> None:
+    """h = res_scale * x_residual + gate * norm(sum of y_slots) * w, optionally with that sum (y)
+    and the next block's x_next = norm(h) * w_next."""
+    _norm_operands("moe_combine_norm", desc,
+                   [("x_residual", x_residual, False), ("h", h, False), ("y", y, True),
+                    ("x_next", x_next, True)], [("w", w, False), ("w_next", w_next, True)],
+                   gates=[("gate", gate, True)], slots=y_slots)
+    _check(_lib.moe_combine_norm(ctypes.byref(desc), _ptr(x_residual), _ptr(y_slots), _ptr(w),
+                                 _ptr(gate), _ptr(w_next), _ptr(h), _ptr(y), _ptr(x_next),
+                                 _stream(stream)), "moe_combine_norm")
+
+
+def moe_norm_backward(desc, x, w, dout, dh, dx, dw, ws, stream=None) -> None:
+    """dx = res_scale * dh + the gradient of x through moe_norm for dout; dw of the weight."""
+    _norm_operands("moe_norm_backward", desc,
+                   [("x", x, False), ("dout", dout, False), ("dh", dh, True), ("dx", dx, False)],
+                   [("w", w, False)], dw=dw, ws=ws)
+    _check(_lib.moe_norm_backward(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(dout), _ptr(dh),
+                                  _ptr(dx), _ptr(dw), _ptr(ws),
+                                  ws.numel() if ws is not None else 0, _stream(stream)),
+           "moe_norm_backward")
+
+
+def moe_combine_norm_backward(desc, y, w, gate, dh, dy, dw, dgate, ws, stream=None) -> None:
+    """Gradients of y, w and the gate through moe_combine_norm's h for dh."""
+    _norm_operands("moe_combine_norm_backward", desc,
+                   [("y", y, False), ("dh", dh, False), ("dy", dy, False)], [("w", w, False)],
+                   dw=dw, gates=[("gate", gate, True), ("dgate", dgate, True)], ws=ws)
+    _check(_lib.moe_combine_norm_backward(ctypes.byref(desc), _ptr(y), _ptr(w), _ptr(gate),
+                                          _ptr(dh), _ptr(dy), _ptr(dw), _ptr(dgate), _ptr(ws),
+                                          ws.numel() if ws is not None else 0, _stream(stream)),
+           "moe_combine_norm_backward")

@@ -2309,3 +2309,5 @@ moe_status moe_ipc_close(void* dev_ptr) {
 }
 
 }  // extern "C"
+
+#include "norm_api.cuh"

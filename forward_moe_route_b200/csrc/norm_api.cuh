@@ -1,0 +1,283 @@
+// Entry points of the block norms: argument checks, the shape rule and the
+// launches.  Included by api.cu, whose helpers it uses.
+#pragma once
+
+#include "norm.cuh"
+
+namespace {
+
+struct NormDims {
+  int64_t T, d;
+  bool bf16;
+  int vec;          // elements of a 16-byte vector
+  int64_t n_gate;   // gate rows (0 without gate)
+};
+
+moe_status norm_dims(const moe_norm_desc* s, NormDims* D) {
+  if (!s) return MOE_ERR_INVALID_ARG;
+  if (s->T < 0 || s->d < 1 || s->d > 65536 || s->n_slots < 1 ||
+      s->n_slots > route::MAXK + kMaxShared || s->gate_group < 0 ||
+      (s->act_dtype != MOE_DT_F32 && s->act_dtype != MOE_DT_BF16))
+    return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(s->eps) || !(s->eps > 0.f) || !std::isfinite(s->res_scale))
+    return MOE_ERR_INVALID_ARG;
+  D->T = s->T;
+  D->d = s->d;
+  D->bf16 = s->act_dtype == MOE_DT_BF16;
+  D->vec = D->bf16 ? 8 : 4;
+  D->n_gate = s->gate_group ? (D->T + s->gate_group - 1) / s->gate_group : 0;
+  return MOE_OK;
+}
+
+// How a row is held.  Rows of whole 16-byte vectors are read in vectors
+// (V = 8 bf16 or 4 fp32), others in single elements; a row of up to 128
+// vectors (64 in the backward) belongs to one warp, a longer one to a block
+// with up to `vpt` vectors a thread; rows beyond that take the looping kernels
+// (vpt = 0).
+struct NormShape {
+  int v, vpt, tpr, threads;
+  int rows_here() const { return threads / tpr; }
+};
+
+NormShape norm_shape(const NormDims& D, bool backward) {
+  NormShape s;
+  const bool whole = D.d % D.vec == 0;
+  s.v = whole ? D.vec : 1;
+  const int64_t n = D.d / s.v;
+  if (whole && n <= (backward ? 64 : 128)) {
+    s.vpt = n <= 32 ? 1 : n <= 64 ? 2 : 4;
+    s.tpr = 32;
+    s.threads = 256;
+    return s;
+  }
+  // the backward keeps the sums of its columns in registers too: 16 elements a
+  // thread at most, in blocks of up to 512 threads
+  const int widest = whole ? (backward ? 16 / D.vec : 4) : 8;
+  const int most = backward && whole && D.vec * widest > 8 ? 512 : norm::MAX_THREADS;
+  s.vpt = whole ? 2 : 8;
+  if (n > (int64_t)s.vpt * most) s.vpt = widest;
+  if (n > (int64_t)s.vpt * most) {
+    s.vpt = 0;
+    s.tpr = s.threads = norm::MAX_THREADS;
+    return s;
+  }
+  s.tpr = (int)((n + s.vpt - 1) / s.vpt + 31) / 32 * 32;
+  s.threads = s.tpr;
+  return s;
+}
+
+// How the backward cuts the tokens: units of `rows` tokens, none across two
+// gate rows, about NORM_BLOCKS of them; a gate row of more tokens is split.
+constexpr int64_t NORM_BLOCKS = 592;   // four blocks for each of 148 SMs
+struct NormCut {
+  int64_t group, rows, split, units, blocks;
+};
+NormCut norm_cut(const NormDims& D, int64_t gate_group, int rows_here) {
+  NormCut c;
+  c.group = gate_group && gate_group < D.T ? gate_group : D.T;
+  const int64_t most = (D.T + NORM_BLOCKS - 1) / NORM_BLOCKS;
+  c.rows = most > rows_here ? most : rows_here;
+  if (c.rows > c.group) c.rows = c.group;
+  if (c.group == 0) {
+    c = NormCut{0, 0, 1, 0, 0};
+    return c;
+  }
+  c.split = (c.group + c.rows - 1) / c.rows;
+  c.units = (D.T + c.group - 1) / c.group * c.split;
+  c.blocks = c.units < NORM_BLOCKS ? c.units : NORM_BLOCKS;
+  return c;
+}
+
+struct NormLayout {
+  size_t part_w, part_g, total;
+};
+NormLayout norm_layout(const NormDims& D, const NormCut& c, bool wide) {
+  NormLayout L;
+  const size_t row = (size_t)D.d * 4;
+  L.part_w = 0;
+  L.part_g = align_up((size_t)c.blocks * row, kAlign);
+  const size_t g = !D.n_gate ? 0 : c.split > 1 ? (size_t)c.units : wide ? (size_t)c.blocks : 0;
+  L.total = align_up(L.part_g + g * row, kAlign);
+  if (!L.total) L.total = kAlign;
+  return L;
+}
+
+template <typename E, bool COMBINE>
+moe_status launch_norm_fwd(const NormShape& s, norm::FwdArgs a, int sms, cudaStream_t st) {
+  constexpr int VEC = norm::Elem<E>::VEC;
+  auto* k = s.v == 1 ? (s.vpt ? norm::k_norm_fwd<E, 1, 8, COMBINE>
+                              : norm::k_norm_fwd_wide<E, 1, COMBINE>)
+            : s.vpt == 1 ? norm::k_norm_fwd<E, VEC, 1, COMBINE>
+            : s.vpt == 2 ? norm::k_norm_fwd<E, VEC, 2, COMBINE>
+            : s.vpt == 4 ? norm::k_norm_fwd<E, VEC, 4, COMBINE>
+                         : norm::k_norm_fwd_wide<E, VEC, COMBINE>;
+  a.tpr = s.tpr;
+  const int64_t blocks = (a.T + s.rows_here() - 1) / s.rows_here();
+  const int64_t most = (int64_t)sms * (2048 / s.threads);
+  return launch_chain(COMBINE ? "k_norm_fwd (combine)" : "k_norm_fwd", k,
+                      dim3((unsigned)(blocks < most ? blocks : most)), dim3(s.threads), 0, st, a);
+}
+
+template <typename E, bool GATE>
+moe_status launch_norm_bwd(const NormShape& s, const NormCut& c, norm::BwdArgs a, float* dw,
+                           cudaStream_t st) {
+  constexpr int VEC = norm::Elem<E>::VEC;
+  if (a.T > 0) {
+    auto* k = s.v == 1 ? (s.vpt ? norm::k_norm_bwd<E, 1, 8, GATE>
+                                : norm::k_norm_bwd_wide<E, 1, GATE>)
+              : s.vpt == 1 ? norm::k_norm_bwd<E, VEC, 1, GATE>
+              : s.vpt == 2 ? norm::k_norm_bwd<E, VEC, 2, GATE>
+              : s.vpt == 4 ? norm::k_norm_bwd<E, VEC, 16 / VEC, GATE>
+                           : norm::k_norm_bwd_wide<E, VEC, GATE>;
+    a.tpr = s.tpr;
+    const size_t smem = s.rows_here() > 1 ? (size_t)s.rows_here() * a.d * 4 : 0;
+    const moe_status rc = launch_chain("k_norm_bwd", k, dim3((unsigned)c.blocks),
+                                       dim3(s.threads), smem, st, a);
+    if (rc != MOE_OK) return rc;
+  }
+  const int64_t gates = GATE && c.split > 1 ? c.units / c.split : 0;
+  return launch_chain("k_norm_join", norm::k_norm_join<E>,
+                      dim3((unsigned)((a.d + 31) / 32), (unsigned)(1 + gates)), dim3(32, 32), 0,
+                      st, static_cast<const float*>(a.part_w), (int)c.blocks, dw,
+                      static_cast<const float*>(a.part_g), (int)c.split,
+                      static_cast<const E*>(a.w), static_cast<E*>(a.dgate), a.d);
+}
+
+moe_status norm_backward(const moe_norm_desc& desc, const NormDims& D, bool with_gate,
+                         norm::BwdArgs a, float* dw, void* ws, size_t ws_bytes,
+                         cudaStream_t st) {
+  const NormShape s = norm_shape(D, true);
+  const NormCut c = norm_cut(D, with_gate ? desc.gate_group : 0, s.rows_here());
+  NormDims Dg = D;
+  if (!with_gate) Dg.n_gate = 0;
+  const NormLayout L = norm_layout(Dg, c, s.vpt == 0);
+  if (!ws || ws_bytes < L.total || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+  int sms;
+  const moe_status rc = device_setup(&sms);
+  if (rc != MOE_OK) return rc;
+  a.part_w = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.part_w);
+  a.part_g = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.part_g);
+  a.T = (int)D.T;
+  a.d = (int)D.d;
+  a.group = (int)c.group;
+  a.rows = (int)c.rows;
+  a.split = (int)c.split;
+  a.units = (int)c.units;
+  a.eps = desc.eps;
+  a.res = desc.res_scale;
+  if (D.bf16)
+    return with_gate ? launch_norm_bwd<__nv_bfloat16, true>(s, c, a, dw, st)
+                     : launch_norm_bwd<__nv_bfloat16, false>(s, c, a, dw, st);
+  return with_gate ? launch_norm_bwd<float, true>(s, c, a, dw, st)
+                   : launch_norm_bwd<float, false>(s, c, a, dw, st);
+}
+
+// a required pointer: present and 16-byte aligned
+inline bool given(const void* p) { return p && aligned16(p); }
+inline bool given_or_null(const void* p) { return aligned16(p); }
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_norm(const moe_norm_desc* desc, const void* x, const void* w, void* out,
+                    cudaStream_t stream) {
+  NormDims D;
+  moe_status rc = norm_dims(desc, &D);
+  if (rc != MOE_OK) return rc;
+  if (D.T == 0) return MOE_OK;
+  if (!given(x) || !given(w) || !given(out) || out == x || out == w) return MOE_ERR_INVALID_ARG;
+  int sms;
+  if ((rc = device_setup(&sms)) != MOE_OK) return rc;
+  norm::FwdArgs a;
+  memset(&a, 0, sizeof(a));
+  a.u = x; a.w = w; a.h = out;
+  a.T = (int)D.T; a.d = (int)D.d; a.S = 1; a.eps = desc->eps;
+  const NormShape s = norm_shape(D, false);
+  return D.bf16 ? launch_norm_fwd<__nv_bfloat16, false>(s, a, sms, stream)
+                : launch_norm_fwd<float, false>(s, a, sms, stream);
+}
+
+moe_status moe_combine_norm(const moe_norm_desc* desc, const void* x_residual,
+                            const void* y_slots, const void* w, const void* gate,
+                            const void* w_next, void* h, void* y, void* x_next,
+                            cudaStream_t stream) {
+  NormDims D;
+  moe_status rc = norm_dims(desc, &D);
+  if (rc != MOE_OK) return rc;
+  if (!w_next != !x_next || !gate != !desc->gate_group) return MOE_ERR_INVALID_ARG;
+  if (D.T == 0) return MOE_OK;
+  if (!given(x_residual) || !given(y_slots) || !given(w) || !given(h) || !given_or_null(gate) ||
+      !given_or_null(w_next) || !given_or_null(y) || !given_or_null(x_next))
+    return MOE_ERR_INVALID_ARG;
+  // outputs apart from the inputs and from one another
+  const void* out[3] = {h, y, x_next};
+  const void* in[5] = {x_residual, y_slots, w, gate, w_next};
+  for (int i = 0; i < 3; ++i) {
+    if (!out[i]) continue;
+    for (const void* p : in)
+      if (p == out[i]) return MOE_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 3; ++j)
+      if (out[j] == out[i]) return MOE_ERR_INVALID_ARG;
+  }
+  int sms;
+  if ((rc = device_setup(&sms)) != MOE_OK) return rc;
+  norm::FwdArgs a;
+  memset(&a, 0, sizeof(a));
+  a.u = x_residual; a.slots = y_slots; a.w = w; a.gate = gate; a.w_next = w_next;
+  a.h = h; a.y = y; a.x_next = x_next;
+  a.T = (int)D.T; a.d = (int)D.d; a.S = desc->n_slots; a.gate_group = desc->gate_group;
+  a.eps = desc->eps; a.res = desc->res_scale;
+  const NormShape s = norm_shape(D, false);
+  return D.bf16 ? launch_norm_fwd<__nv_bfloat16, true>(s, a, sms, stream)
+                : launch_norm_fwd<float, true>(s, a, sms, stream);
+}
+
+size_t moe_norm_backward_workspace_size(const moe_norm_desc* desc) {
+  NormDims D;
+  if (norm_dims(desc, &D) != MOE_OK) return 0;
+  const NormShape s = norm_shape(D, true);
+  NormDims plain = D;
+  plain.n_gate = 0;
+  const size_t without =
+      norm_layout(plain, norm_cut(D, 0, s.rows_here()), s.vpt == 0).total;
+  const size_t with =
+      norm_layout(D, norm_cut(D, desc->gate_group, s.rows_here()), s.vpt == 0).total;
+  return with > without ? with : without;
+}
+
+moe_status moe_norm_backward(const moe_norm_desc* desc, const void* x, const void* w,
+                             const void* dout, const void* dh, void* dx, float* dw, void* ws,
+                             size_t ws_bytes, cudaStream_t stream) {
+  NormDims D;
+  moe_status rc = norm_dims(desc, &D);
+  if (rc != MOE_OK) return rc;
+  if (!given(dw)) return MOE_ERR_INVALID_ARG;
+  if (D.T > 0 && (!given(x) || !given(w) || !given(dout) || !given_or_null(dh) || !given(dx) ||
+                  dx == x || dx == w || dx == dout || dx == dh))
+    return MOE_ERR_INVALID_ARG;
+  norm::BwdArgs a;
+  memset(&a, 0, sizeof(a));
+  a.v = x; a.w = w; a.up = dout; a.add = dh; a.dv = dx;
+  return norm_backward(*desc, D, false, a, dw, ws, ws_bytes, stream);
+}
+
+moe_status moe_combine_norm_backward(const moe_norm_desc* desc, const void* y, const void* w,
+                                     const void* gate, const void* dh, void* dy, float* dw,
+                                     void* dgate, void* ws, size_t ws_bytes,
+                                     cudaStream_t stream) {
+  NormDims D;
+  moe_status rc = norm_dims(desc, &D);
+  if (rc != MOE_OK) return rc;
+  if (!given(dw) || !gate != !desc->gate_group || !gate != !dgate) return MOE_ERR_INVALID_ARG;
+  if (D.T > 0 && (!given(y) || !given(w) || !given_or_null(gate) || !given(dh) || !given(dy) ||
+                  !given_or_null(dgate) || dy == y || dy == w || dy == gate || dy == dh ||
+                  dy == dgate || (gate && dgate == gate)))
+    return MOE_ERR_INVALID_ARG;
+  norm::BwdArgs a;
+  memset(&a, 0, sizeof(a));
+  a.v = y; a.w = w; a.gate = gate; a.up = dh; a.dv = dy; a.dgate = dgate;
+  return norm_backward(*desc, D, gate != nullptr, a, dw, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

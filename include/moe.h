@@ -490,6 +490,68 @@ moe_status moe_quantize_fp8_blockwise_t(const void* w_bf16, int32_t rows, int32_
                                         int32_t batch, void* w_e4m3_t, float* scale_t,
                                         cudaStream_t stream);
 
+/* ---- Norms around the layer ------------------------------------------------
+ * Before the layer x = u r(u) w with r(v) = (mean(v^2) + eps)^-1/2, the x that
+ * moe_forward takes beside x_residual = u; behind it, in one pass,
+ *   y = sum_s y_slots[t, s],   h = res_scale u + gate * (y r(y) w),
+ *   x_next = h r(h) w_next     (the next block's norm; optional)
+ * and the backward passes of both.  fp32 arithmetic; each output rounded once
+ * (x_next from the unrounded h, y r(y) from the unrounded sum).
+ *   u, y, h, x, gradients of them: [T, d] act_dtype;  w, w_next [d] act_dtype
+ *   gate [ceil(T / gate_group), d] act_dtype: token t takes row t / gate_group,
+ *     so gate_group = 1 is a gate per token, gate_group >= T one per channel,
+ *     between them one per run of tokens; gate NULL exactly when gate_group = 0
+ *   dw, the gradient of w: [d] fp32
+ * Outputs must not overlap the inputs or one another; an output at an input's
+ * address is refused.  Any d from 1 to 65536 is accepted; rows of whole
+ * 16-byte vectors (d a multiple of 8 in bf16, 4 in fp32) run fastest.  Two
+ * runs on the same inputs give the same bits. */
+typedef struct moe_norm_desc {
+  int32_t T;           /* tokens, >= 0 */
+  int32_t d;           /* hidden size, 1..65536 */
+  int32_t n_slots;     /* rows of y_slots a token, 1..80 (moe_combine_norm only) */
+  int32_t gate_group;  /* tokens that share a gate row; 0: no gate */
+  int32_t act_dtype;   /* MOE_DT_F32 or MOE_DT_BF16 */
+  float eps;           /* > 0 */
+  float res_scale;     /* of the residual */
+} moe_norm_desc;
+
+/* out = x r(x) w (T, d, act_dtype and eps of desc). */
+moe_status moe_norm(const moe_norm_desc* desc, const void* x, const void* w, void* out,
+                    cudaStream_t stream);
+
+/* End of a block from the expert rows of moe_grouped_swiglu (n_slots = K + Ks)
+ * or from a layer output without residual (n_slots = 1).
+ *   y_slots [T, n_slots, d];  y [T, d] out or NULL: the sum, rounded, as the
+ *   backward reads it;  w_next and x_next both given or both NULL. */
+moe_status moe_combine_norm(const moe_norm_desc* desc, const void* x_residual,
+                            const void* y_slots, const void* w, const void* gate,
+                            const void* w_next, void* h, void* y, void* x_next,
+                            cudaStream_t stream);
+
+/* Bytes of workspace either backward needs (0 if desc is invalid). */
+size_t moe_norm_backward_workspace_size(const moe_norm_desc* desc);
+
+/* Backward of moe_norm joined with the residual's gradient: with c = dout * w,
+ *   dx = res_scale dh + r c - x r^3 mean(x c),   dw = sum_t dout * x r,
+ * dh [T, d] the gradient of the block's output h, or NULL for none.  The
+ * gradient of moe_combine_norm's x_next flows through this call with x = h. */
+moe_status moe_norm_backward(const moe_norm_desc* desc, const void* x, const void* w,
+                             const void* dout, const void* dh, void* dx, float* dw, void* ws,
+                             size_t ws_bytes, cudaStream_t stream);
+
+/* Backward of moe_combine_norm's h for dh = dL/dh: with n = y r(y) and
+ * c = dh * gate * w,
+ *   dy = r c - y r^3 mean(y c) (the gradient of every slot of a token: the dh
+ *   of moe_backward),  dw = sum_t dh * gate * n,
+ *   dgate = sum over the gate row's tokens of dh * w * n, rounded once.
+ *   y as moe_combine_norm wrote it; gate, dgate NULL exactly when gate_group
+ *   = 0.  The residual's gradient, res_scale dh, is left to moe_norm_backward. */
+moe_status moe_combine_norm_backward(const moe_norm_desc* desc, const void* y, const void* w,
+                                     const void* gate, const void* dh, void* dy, float* dw,
+                                     void* dgate, void* ws, size_t ws_bytes,
+                                     cudaStream_t stream);
+
 /* Human-readable name of a status. */
 const char* moe_status_string(moe_status status);
 

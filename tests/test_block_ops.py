@@ -1,0 +1,138 @@
+"""The operators around the layer, what needs no GPU: the fp64 oracle's
+gradients against differences, and the refusals of the entry points."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import forward_moe_route_b200 as moe
+from oracle import block
+
+
+def differences(f, x, e=1e-6):
+    """df/dx of a scalar function by central differences."""
+    g = np.zeros_like(x)
+    for i in np.ndindex(*x.shape):
+        keep = x[i]
+        x[i] = keep + e
+        up = f()
+        x[i] = keep - e
+        down = f()
+        x[i] = keep
+        g[i] = (up - down) / (2 * e)
+    return g
+
+
+# central differences of step e = 1e-6 of functions of order 10: the rounding of f, 1e-15 * 10,
+# over e leaves 1e-8, the truncation e^2 less
+DIFF = 1e-6
+
+
+@pytest.mark.parametrize("gate_group", [0, 1, 2, 100])
+def test_oracle_norm_gradients_against_differences(gate_group):
+    rng = np.random.default_rng(gate_group)
+    T, d, eps, res = 5, 6, 1e-2, 0.7
+    u, ys = rng.normal(size=(T, d)), rng.normal(size=(T, 3, d))
+    w, wn = 1 + 0.2 * rng.normal(size=d), 1 + 0.2 * rng.normal(size=d)
+    gate = rng.normal(size=(-(-T // gate_group), d)) if gate_group else None
+    gh, gx = rng.normal(size=(T, d)), rng.normal(size=(T, d))
+
+    def loss():
+        h, _, xn = block.combine_norm(u, ys, w, gate, gate_group, res, wn, eps)
+        return np.sum(gh * h) + np.sum(gx * xn)
+
+    h, y, _ = block.combine_norm(u, ys, w, gate, gate_group, res, wn, eps)
+    dh, dwn = block.norm_backward(h, wn, gx, gh, 1.0, eps)
+    dy, dw, dgate = block.combine_norm_backward(y, w, gate, gate_group, dh, eps)
+    np.testing.assert_allclose(differences(loss, u), res * dh, atol=DIFF)
+    np.testing.assert_allclose(differences(loss, ys), np.repeat(dy[:, None], 3, 1), atol=DIFF)
+    np.testing.assert_allclose(differences(loss, w), dw, atol=DIFF)
+    np.testing.assert_allclose(differences(loss, wn), dwn, atol=DIFF)
+    if gate_group:
+        np.testing.assert_allclose(differences(loss, gate), dgate, atol=DIFF)
+
+
+def norm_desc(**kw):
+    base = dict(T=16, d=256, eps=1e-6, dtype="bf16", n_slots=2, gate_group=4, res_scale=1.0)
+    base.update(kw)
+    return moe.make_norm_desc(**base)
+
+
+@pytest.mark.parametrize("kw", [dict(T=-1), dict(d=0), dict(d=65537), dict(n_slots=0),
+                                dict(n_slots=81), dict(gate_group=-1), dict(eps=0.0),
+                                dict(eps=float("nan")), dict(eps=float("inf")),
+                                dict(res_scale=float("inf"))])
+def test_invalid_norm_descriptors(kw):
+    d = norm_desc(**kw)
+    L = moe.lib()
+    assert moe.moe_norm_backward_workspace_size(d) == 0
+    r = ctypes.byref(d)
+    assert L.moe_norm(r, 16, 32, 48, None) == moe.ERR_INVALID_ARG
+    assert L.moe_combine_norm(r, 16, 32, 48, 64, 80, 96, 112, 128, None) == moe.ERR_INVALID_ARG
+    assert L.moe_norm_backward(r, 16, 32, 48, 64, 80, 96, 112, 1 << 30,
+                               None) == moe.ERR_INVALID_ARG
+    assert L.moe_combine_norm_backward(r, 16, 32, 48, 64, 80, 96, 112, 128, 1 << 30,
+                                       None) == moe.ERR_INVALID_ARG
+
+
+def test_norm_struct_matches_header_layout():
+    assert ctypes.sizeof(moe.MoeNormDesc) == 7 * 4
+    d = norm_desc()
+    d.act_dtype = moe.DT_E4M3
+    assert moe.moe_norm_backward_workspace_size(d) == 0
+
+
+def test_norm_entry_points_reject_before_touching_cuda():
+    L = moe.lib()
+    d = norm_desc()
+    r, bad = ctypes.byref(d), moe.ERR_INVALID_ARG
+    plain = norm_desc(gate_group=0)
+    p = ctypes.byref(plain)
+    # missing, misaligned, and an output at an input's address
+    assert L.moe_norm(r, None, 32, 48, None) == bad
+    assert L.moe_norm(r, 16, 33, 48, None) == bad
+    assert L.moe_norm(r, 16, 32, 16, None) == bad
+    ok = [16, 32, 48, 64, 80, 96, 112, 128]
+    for i in (0, 1, 2, 5):
+        assert L.moe_combine_norm(r, *ok[:i], None, *ok[i + 1:], None) == bad, i
+    for i in range(8):
+        assert L.moe_combine_norm(r, *ok[:i], ok[i] + 2, *ok[i + 1:], None) == bad, i
+    # a gate without gate_group, gate_group without a gate
+    assert L.moe_combine_norm(p, *ok, None) == bad
+    assert L.moe_combine_norm(r, 16, 32, 48, None, 80, 96, 112, 128, None) == bad
+    # w_next without x_next and the other way round
+    assert L.moe_combine_norm(r, 16, 32, 48, 64, None, 96, 112, 128, None) == bad
+    assert L.moe_combine_norm(r, 16, 32, 48, 64, 80, 96, 112, None, None) == bad
+    # outputs on inputs and on one another
+    for i in range(5):
+        assert L.moe_combine_norm(r, *ok[:5], ok[i], 112, 128, None) == bad, i
+    assert L.moe_combine_norm(r, *ok[:5], 96, 96, 128, None) == bad
+    assert L.moe_combine_norm(r, *ok[:5], 96, 112, 112, None) == bad
+    # backward
+    big = 1 << 30
+    for i in (0, 1, 2, 4, 5):
+        a = [16, 32, 48, 64, 80, 96]
+        a[i] = None
+        assert L.moe_norm_backward(r, *a, 112, big, None) == bad, i
+    assert L.moe_norm_backward(r, 16, 32, 48, 64, 64, 96, 112, big, None) == bad
+    assert L.moe_norm_backward(r, 16, 32, 48, 64, 80, 96, None, big, None) == moe.ERR_WORKSPACE
+    assert L.moe_norm_backward(r, 16, 32, 48, 64, 80, 96, 112, 16, None) == moe.ERR_WORKSPACE
+    assert L.moe_combine_norm_backward(r, 16, 32, None, 64, 80, 96, 112, 128, big, None) == bad
+    assert L.moe_combine_norm_backward(r, 16, 32, 48, 64, 80, 96, None, 128, big, None) == bad
+    assert L.moe_combine_norm_backward(p, 16, 32, 48, 64, 80, 96, 112, 128, big, None) == bad
+    assert L.moe_combine_norm_backward(r, 16, 32, 48, 64, 80, 96, 48, 128, big, None) == bad
+    assert L.moe_combine_norm_backward(r, 16, 32, 48, 64, 80, 96, 112, 128, 16,
+                                       None) == moe.ERR_WORKSPACE
+
+
+def test_norm_binding_refuses():
+    import torch
+    d = norm_desc(gate_group=0)
+    x = torch.zeros(16, 256, dtype=torch.bfloat16)
+    w = torch.zeros(256, dtype=torch.bfloat16)
+    for args, what in [((x[:15], w, x), "holds"), ((x.t(), w, x), "contiguous"),
+                       ((x.float(), w, x), "float32"), ((x, None, x), "missing"),
+                       ((x, w, x), "CUDA")]:
+        with pytest.raises(moe.MoeError, match=what) as e:
+            moe.moe_norm(d, *args)
+        assert e.value.status == moe.ERR_INVALID_ARG
