@@ -130,6 +130,10 @@ _SIGS = {
     "moe_norm_backward": (ctypes.c_int, [_ND, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_combine_norm_backward": (ctypes.c_int, [_ND, _P, _P, _P, _P, _P, _P, _P, _P,
                                                  ctypes.c_size_t, _P]),
+    "moe_grouped_mm": (ctypes.c_int, [ctypes.c_int32] * 4 + [_P] * 5),
+    "moe_grouped_mm_dx": (ctypes.c_int, [ctypes.c_int32] * 4 + [_P] * 5),
+    "moe_grouped_mm_dw": (ctypes.c_int, [ctypes.c_int32] * 4 + [_P] * 4 + [ctypes.c_int32] * 2 +
+                          [_P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -789,3 +793,48 @@ def moe_combine_norm_backward(desc, y, w, gate, dh, dy, dw, dgate, ws, stream=No
                                           _ptr(dh), _ptr(dy), _ptr(dw), _ptr(dgate), _ptr(ws),
                                           ws.numel() if ws is not None else 0, _stream(stream)),
            "moe_combine_norm_backward")
+
+
+def _grouped_operands(where: str, offsets, rows_in, weights, dtypes, **rows) -> tuple:
+    """Check the tensors of a grouped product; (n_groups, n_rows, d_in, d_out).  rows_in and
+    `rows`: name -> (tensor, "in" or "out") of [n_rows, d_in or d_out]; weights: (name, tensor)."""
+    wname, w = weights
+    if w.dim() != 3:
+        raise MoeError(ERR_INVALID_ARG, f"{where}: {wname} must be [n_groups, d_out, d_in]")
+    G, d_out, d_in = w.shape
+    n_rows = rows_in.shape[0]
+    _operand(where, wname, w, w.numel(), dtypes)
+    _operand(where, "offsets", offsets, G + 1, ("int32",))
+    for name, (t, side) in rows.items():
+        width = d_in if side == "in" else d_out
+        if t.dim() != 2 or tuple(t.shape) != (n_rows, width):
+            raise MoeError(ERR_INVALID_ARG, f"{where}: {name} must be [{n_rows}, {width}]")
+        _operand(where, name, t, n_rows * width, ("bfloat16",))
+    _on_device(where, [(wname, w), ("offsets", offsets)] + [(k, v[0]) for k, v in rows.items()])
+    return G, n_rows, d_in, d_out
+
+
+def moe_grouped_mm(x, w, offsets, y, stream=None) -> None:
+    """y[r] = w[g] @ x[r] for the rows offsets[g] <= r < offsets[g + 1] of every group g."""
+    dims = _grouped_operands("moe_grouped_mm", offsets, x, ("w", w), ("bfloat16",), x=(x, "in"),
+                             y=(y, "out"))
+    _check(_lib.moe_grouped_mm(*dims, _ptr(x), _ptr(w), _ptr(offsets), _ptr(y),
+                               _stream(stream)), "moe_grouped_mm")
+
+
+def moe_grouped_mm_dx(dy, w, offsets, dx, stream=None) -> None:
+    """dx[r] = w[g].T @ dy[r]: the gradient of moe_grouped_mm's rows."""
+    dims = _grouped_operands("moe_grouped_mm_dx", offsets, dy, ("w", w), ("bfloat16",),
+                             dy=(dy, "out"), dx=(dx, "in"))
+    _check(_lib.moe_grouped_mm_dx(*dims, _ptr(dy), _ptr(w), _ptr(offsets), _ptr(dx),
+                                  _stream(stream)), "moe_grouped_mm_dx")
+
+
+def moe_grouped_mm_dw(dy, x, offsets, dw, accumulate: bool = False, stream=None) -> None:
+    """dw[g] = sum of dy[r] x[r]^T over the group's rows (fp32 or bf16 by dw's type); with
+    accumulate (fp32 only) added to dw."""
+    dims = _grouped_operands("moe_grouped_mm_dw", offsets, dy, ("dw", dw),
+                             ("float32", "bfloat16"), dy=(dy, "out"), x=(x, "in"))
+    _check(_lib.moe_grouped_mm_dw(*dims, _ptr(dy), _ptr(x), _ptr(offsets), _ptr(dw),
+                                  int(dw.element_size() == 2), int(accumulate),
+                                  _stream(stream)), "moe_grouped_mm_dw")

@@ -20,6 +20,7 @@
 #include "bwd.cuh"
 #include "bwd8.cuh"
 #include "gemm_bwd.cuh"
+#include "grouped.cuh"
 
 using namespace moe;
 
@@ -116,10 +117,11 @@ struct DeviceInfo {
   int sms = 0;
   bool attrs_done = false;
   // co-resident 2-CTA clusters of the pair GEMMs (0: gate/up, 1: down,
-  // 2: backward weight gradients, 3: backward activation GEMMs), and the
-  // dynamic shared memory each count was taken for
-  size_t pair_smem[4] = {0, 0, 0, 0};
-  int pair_clusters[4] = {0, 0, 0, 0};
+  // 2: backward weight gradients, 3: backward activation GEMMs, 4 and 5:
+  // grouped products and their row gradients, 6 and 7: their weight gradients
+  // in fp32 and bf16), and the dynamic shared memory each count was taken for
+  size_t pair_smem[8] = {};
+  int pair_clusters[8] = {};
 };
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
@@ -176,6 +178,18 @@ moe_status device_setup(int* sms) {
                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(gemm8::k_gemm_promoted<2, gemm8::EPI_BF16_OUT, true>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(grouped::k_grouped_mm<false>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(grouped::k_grouped_mm<true>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(grouped::k_grouped_dw<false>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(grouped::k_grouped_dw<true>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (dynamic shared memory)");
     // the promoted GEMMs re-split their registers with setmaxnreg; the split
@@ -2311,3 +2325,4 @@ moe_status moe_ipc_close(void* dev_ptr) {
 }  // extern "C"
 
 #include "norm_api.cuh"
+#include "grouped_api.cuh"

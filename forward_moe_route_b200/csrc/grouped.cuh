@@ -1,0 +1,620 @@
+// Products grouped by expert over a ragged row list, with their gradients, on
+// tcgen05 / TMEM, fed by TMA, on CTA pairs (tcgen05.mma.cta_group::2).
+//
+//   rows of group g: offsets[g] .. offsets[g+1] - 1, anywhere in the row list
+//   y_r  = W_g x_r              k_grouped_mm<false>   (contracts over d_in)
+//   dx_r = W_g^T dy_r           k_grouped_mm<true>    (contracts over d_out)
+//   dW_g = sum_r dy_r x_r^T     k_grouped_dw          (contracts over the rows)
+//
+// All operands bf16, accumulation fp32 in TMEM over the whole contraction.
+//
+// k_grouped_mm computes D = (weights) x (rows)^T: 256 features on the UMMA M
+// side, up to 256 rows of one group on the N side, so a group of few rows
+// costs few columns and streams its weights once.  The weights are addressed
+// through a three-dimensional tensor map [G, d_out, d_in], so a tile's edge is
+// filled with zeros instead of the next expert's weights; for dx they are read
+// MN-major (gemm_bwd.cuh), not transposed in memory.  Rows of the next group
+// that a row tile brings along only reach accumulator columns nobody stores.
+//
+// k_grouped_dw has the ragged rows on the contraction side, where the next
+// group's rows must not enter the sum, and zeros in one operand would not
+// cancel a NaN in the other.  Rows are taken 64 a stage and 16 per UMMA; of a
+// group's last stage only the 16-row steps that hold rows are issued, and in
+// the last step the shared-memory lines behind the group's end are overwritten
+// with zeros in both operands: that stage's copies complete on a barrier of
+// their own in each CTA (one per stage), warp 3 clears the lines (fewer than 16) and then
+// arrives for the stage in the producer's place.  No row is copied or padded in
+// global memory.
+//
+// Every CTA reads the offsets itself (no preparing launch); a group whose offsets decrease or leave [0, n_rows] is reported and
+// treated as empty.
+//
+// Warp roles (384 threads in k_grouped_mm, 256 in k_grouped_dw): warp 0 TMA
+// producer, warp 1 MMA issuer (leader CTA), warp 2 TMEM allocator, warp 3 tail
+// rows (k_grouped_dw), the rest epilogue.  Two accumulators of 256 columns.
+// Barriers and bounded waits as in gemm_t.cuh.
+#pragma once
+
+#include "bulk.cuh"
+#include "common.cuh"
+#include "gemm.cuh"
+#include "gemm_bwd.cuh"
+#include "gemm_t.cuh"
+
+namespace moe {
+namespace grouped {
+
+constexpr int MAX_GROUPS = 1024;
+constexpr int STAGES = 6;
+constexpr uint32_t STAGE_BYTES = 32768;        // 16 KB of either operand per CTA
+constexpr uint32_t HALF_STAGE = STAGE_BYTES / 2;
+constexpr int SMALL_ROWS = 32;                 // rows of the small row box
+constexpr int ACC_COLS = 256;
+constexpr int TMEM_COLS = 512;
+constexpr uint32_t BAR_BYTES = (3 * STAGES + 6) * 8 + 16;
+constexpr uint32_t TAB_BYTES = (3 * MAX_GROUPS + 1) * 4 + 12;
+
+// ---- rows on the N side -------------------------------------------------------------
+constexpr int MM_THREADS = 384;
+constexpr int MM_EPI_WARPS = 8;
+constexpr uint32_t MM_XPOSE = 16 * 32 * 2;     // a warp's 16 rows x 32 features, bf16
+constexpr uint32_t MM_SMEM = 1024 + STAGES * STAGE_BYTES + MM_EPI_WARPS * MM_XPOSE + BAR_BYTES +
+                             TAB_BYTES;
+
+// ---- weight gradients -----------------------------------------------------------------
+constexpr int DW_THREADS = 256;
+constexpr uint32_t DW_STORE = 4 * 2 * 4096;
+constexpr uint32_t DW_SMEM = 1024 + STAGES * STAGE_BYTES + DW_STORE + BAR_BYTES;
+static_assert(MM_SMEM <= 232448 && DW_SMEM <= 232448, "shared memory of one block");
+
+struct Args {
+  const int* offsets;   // [n + 1]
+  int n, n_rows;
+  int feats, contract;  // k_grouped_mm: output features, contraction length
+  int d_out, d_in;      // k_grouped_dw
+  int accumulate;
+  __nv_bfloat16* y;     // k_grouped_mm: [n_rows, feats]
+};
+
+__device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_t bar_cluster,
+                                                 void* smem_dst, int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"((uint64_t)map), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* smem_src, int32_t x,
+                                           int32_t y, int32_t z) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
+      " [%0, {%2, %3, %4}], [%1];" ::"l"((uint64_t)map),
+      "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// rows r0 .. r1 - 1 of a group lie within the row list
+__device__ __forceinline__ bool group_ok(int r0, int r1, int n_rows) {
+  return r0 >= 0 && r1 >= r0 && r1 <= n_rows;
+}
+
+// The group list in shared memory: first row and rows of each group, and the
+// prefix of its row tiles.  One warp builds it.
+struct Groups {
+  int *row0, *rows, *prefix;   // [n], [n], [n + 1]
+  int n;
+  __device__ __forceinline__ Groups(int* base, int count)
+      : row0(base), rows(base + MAX_GROUPS), prefix(base + 2 * MAX_GROUPS), n(count) {}
+  __device__ __forceinline__ void build(const int* offsets, int n_rows, int tile_rows) {
+    const int lane = lane_id();
+    int carry = 0;
+    for (int base = 0; base < n; base += 32) {
+      const int g = base + lane;
+      int r0 = 0, r = 0;
+      if (g < n) {
+        r0 = offsets[g];
+        const int r1 = offsets[g + 1];
+        if (!group_ok(r0, r1, n_rows)) {
+          set_status(MOE_ERR_DEVICE_CHECK);
+          r0 = 0;
+        } else {
+          r = r1 - r0;
+        }
+        row0[g] = r0;
+        rows[g] = r;
+      }
+      const int v = (r + tile_rows - 1) / tile_rows;
+      int incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (g < n) prefix[g] = carry + incl - v;
+      carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) prefix[n] = carry;
+  }
+};
+
+template <bool W_MN>
+__global__ void __launch_bounds__(MM_THREADS, 1)
+    k_grouped_mm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                 const __grid_constant__ CUtensorMap tmXs, const Args a) {
+  using namespace gemmt;   // cluster helpers of the pair kernels
+  constexpr int TF = 256, TR = 256;   // features and rows of a pair's tile
+  constexpr int S = STAGES;
+  grid_dep_sync();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* xpose = smem + S * STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(xpose + MM_EPI_WARPS * MM_XPOSE);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Groups gr(reinterpret_cast<int*>(tmem_slot + 4), a.n);
+
+  const int warp = warp_id(), lane = lane_id();
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  if (warp == 0) gr.build(a.offsets, a.n_rows, TR);
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int j = 0; j < 2; ++j) {
+      mbar_init(&tfull[j], 1);
+      mbar_init(&tempty[j], 2 * MM_EPI_WARPS * 32);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmXs);
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();      // barrier initialisation is visible to the peer from here on
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int n_ft = (a.feats + TF - 1) / TF;
+  const int total = gr.prefix[a.n] * n_ft;
+  const int num_kb = (a.contract + 63) / 64;
+  const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
+
+  // feature tiles run fastest, so the pairs of one wave share a group's rows in L2
+  struct Tile {
+    int g, ft, row, rows, cols;   // group, feature tile, first row, its rows, UMMA N
+  };
+  auto locate = [&](int tile) {
+    Tile t;
+    const int rt = tile / n_ft;
+    t.ft = tile - rt * n_ft;
+    t.g = gemm::find_group(gr.prefix, a.n, rt);
+    const int at = (rt - gr.prefix[t.g]) * TR;
+    t.row = gr.row0[t.g] + at;
+    t.rows = min(TR, gr.rows[t.g] - at);
+    t.cols = (t.rows + 31) & ~31;
+    return t;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer (both CTAs)
+    if (elect_one()) {
+      int it = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < total && ok; tile += tstep) {
+        const Tile t = locate(tile);
+        // a tile of few rows takes them with the small box
+        const bool small = t.cols / 2 <= SMALL_ROWS;
+        const CUtensorMap* tx = small ? &tmXs : &tmX;
+        const uint32_t bytes = HALF_STAGE + (small ? SMALL_ROWS * 128u : HALF_STAGE);
+        const int xrow = t.row + (int)rank * (t.cols / 2);
+        const int f = t.ft * TF + (int)rank * 128;
+        for (int kb = 0; kb < num_kb; ++kb, ++it) {
+          const int s = it % S;
+          const uint32_t ph = (uint32_t)(it / S) & 1u;
+          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag)) { ok = false; break; }
+          uint8_t* sw = smem + (size_t)s * STAGE_BYTES;
+          const uint32_t fl = mapa(smem_u32(&full[s]), 0);
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+          const int k = kb * 64;
+          if (W_MN) {
+            tma_load_3d_pair(&tmW, fl, sw, f, k, t.g);
+            tma_load_3d_pair(&tmW, fl, sw + gbwd::MN_BOX_BYTES, f + 64, k, t.g);
+          } else {
+            tma_load_3d_pair(&tmW, fl, sw, k, f, t.g);
+          }
+          tma_load_2d_pair(tx, fl, sw + HALF_STAGE, k, xrow);
+        }
+      }
+      // the copies this CTA issued land before the block may leave (bounded)
+      volatile int no_abort = 0;
+      for (int j = (it - S > 0 ? it - S : 0); j < it; ++j)
+        mbar_wait(&empty[j % S], (uint32_t)(j / S) & 1u, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer (leader)
+    if (leader && elect_one()) {
+      int it = 0, tcount = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < total && ok; tile += tstep, ++tcount) {
+        const Tile t = locate(tile);
+        const uint32_t idesc = umma_idesc(1, TF, t.cols) | (W_MN ? (1u << 15) : 0u);
+        const int acc = tcount & 1;
+        const uint32_t use = (uint32_t)(tcount >> 1);
+        if (!mbar_wait(&tempty[acc], (use & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
+        for (int kb = 0; kb < num_kb; ++kb, ++it) {
+          const int s = it % S;
+          const uint32_t ph = (uint32_t)(it / S) & 1u;
+          if (!mbar_wait(&full[s], ph, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sw = smem_u32(smem + (size_t)s * STAGE_BYTES);
+          const uint64_t wd = W_MN ? gbwd::umma_desc_sw128_mn(sw) : umma_desc_sw128(sw);
+          const uint64_t xd = umma_desc_sw128(sw + HALF_STAGE);
+          constexpr uint64_t w_step = W_MN ? (2048 >> 4) : (32 >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_pair<0>(d_tmem, wd + w_step * k, xd + (uint64_t)(2 * k), idesc,
+                         (kb | k) != 0 ? 1u : 0u);
+          const uint32_t e_local = smem_u32(&empty[s]);
+          umma_commit_pair(mapa(e_local, 0));
+          umma_commit_pair(mapa(e_local, 1));
+        }
+        if (ok) {
+          const uint32_t t_local = smem_u32(&tfull[acc]);
+          umma_commit_pair(mapa(t_local, 0));
+          umma_commit_pair(mapa(t_local, 1));
+        }
+      }
+      umma_commit_pair(mapa(smem_u32(drain), 0));
+      volatile int no_abort = 0;
+      mbar_wait(drain, 0, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ epilogue (both CTAs)
+    // Warp w reads TMEM lanes 32 (w % 4) .. +31 (32 features) and every other
+    // chunk of 16 rows; a chunk is transposed in shared memory and stored as
+    // 64 bytes per row.
+    const int ew = warp - 4, q = warp & 3, par = ew >> 2;
+    uint8_t* xb = xpose + (size_t)ew * MM_XPOSE;
+    const uint32_t tempty_leader0 = mapa(smem_u32(&tempty[0]), 0);
+    const uint32_t tempty_leader1 = mapa(smem_u32(&tempty[1]), 0);
+    int tcount = 0;
+    for (int tile = tile0; tile < total; tile += tstep, ++tcount) {
+      const Tile t = locate(tile);
+      const int acc = tcount & 1;
+      const uint32_t use = (uint32_t)(tcount >> 1);
+      if (!mbar_wait(&tfull[acc], use & 1u, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+      const int f0 = t.ft * TF + (int)rank * 128 + q * 32;
+      for (int c = par; c * 16 < t.rows; c += 2) {
+        float v[16];
+        tmem_ld16(tb + (uint32_t)(16 * c), v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          reinterpret_cast<__nv_bfloat16*>(xb)[j * 32 + lane] = __float2bfloat16_rn(v[j]);
+        __syncwarp();
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int pi = lane + 32 * m, j = pi >> 2, pc = pi & 3;
+          const uint4 val = *reinterpret_cast<const uint4*>(xb + j * 64 + pc * 16);
+          const int r = 16 * c + j, f = f0 + pc * 8;
+          if (r < t.rows && f < a.feats)
+            *reinterpret_cast<uint4*>(a.y + (size_t)(t.row + r) * a.feats + f) = val;
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      if (leader) mbar_arrive(&tempty[acc]);
+      else mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();      // the peer no longer touches this CTA's barriers or TMEM
+  if (warp == 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// dW tile of 256 output features (d_out, the UMMA M side) x 256 input features
+// (d_in); both operands MN-major.  tmC: [G, d_out, d_in], 32 x 32 boxes.
+template <bool OUT_BF16>
+__global__ void __launch_bounds__(DW_THREADS, 1)
+    k_grouped_dw(const __grid_constant__ CUtensorMap tmDy, const __grid_constant__ CUtensorMap tmX,
+                 const __grid_constant__ CUtensorMap tmC, const Args a) {
+  using namespace gemmt;
+  constexpr int TO = 256, TI = 256;
+  constexpr int S = STAGES;
+  constexpr uint32_t BOX = gbwd::MN_BOX_BYTES;    // 64 rows x 64 features
+  static_assert(4 * BOX == STAGE_BYTES, "two boxes of either operand per CTA");
+  grid_dep_sync();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* store_buf = smem + S * STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(store_buf + DW_STORE);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint64_t* tail = drain + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + S);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = warp_id(), lane = lane_id();
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 2);      // both CTAs' producers, or both CTAs' tail warps
+      mbar_init(&empty[s], 1);
+      mbar_init(&tail[s], 1);
+    }
+    for (int j = 0; j < 2; ++j) {
+      mbar_init(&tfull[j], 1);
+      mbar_init(&tempty[j], 2 * 4 * 32);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&tmDy);
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmC);
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int n_it = (a.d_in + TI - 1) / TI, n_ot = (a.d_out + TO - 1) / TO;
+  const int per_group = n_it * n_ot;
+  const int total = a.n * per_group;
+  const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
+
+  struct Tile {
+    int g, ot, it, row, rows, nkb, cols;
+  };
+  auto locate = [&](int tile) {
+    Tile t;
+    t.g = tile / per_group;
+    const int l = tile - t.g * per_group;
+    t.ot = l / n_it;
+    t.it = l - t.ot * n_it;
+    t.row = __ldg(a.offsets + t.g);
+    const int end = __ldg(a.offsets + t.g + 1);
+    t.rows = group_ok(t.row, end, a.n_rows) ? end - t.row : 0;
+    t.nkb = (t.rows + 63) / 64;
+    t.cols = (min(TI, a.d_in - t.it * TI) + 31) & ~31;
+    return t;
+  };
+  // nothing to add: every role leaves the tile out
+  auto idle = [&](const Tile& t) { return a.accumulate && t.rows == 0; };
+  // the group's last stage when its rows end inside a 16-row step
+  auto is_tail = [&](const Tile& t, int kb) { return kb == t.nkb - 1 && (t.rows & 15) != 0; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer (both CTAs)
+    if (elect_one()) {
+      int it = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < total && ok; tile += tstep) {
+        const Tile t = locate(tile);
+        if (idle(t)) continue;
+        const int o = t.ot * TO + (int)rank * 128;
+        const int i = t.it * TI + (int)rank * (t.cols / 2);
+        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+          const int s = it % S;
+          const uint32_t ph = (uint32_t)(it / S) & 1u;
+          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag)) { ok = false; break; }
+          uint8_t* sa = smem + (size_t)s * STAGE_BYTES;
+          const int r = t.row + kb * 64;
+          if (is_tail(t, kb)) {
+            mbar_arrive_expect_tx(&tail[s], STAGE_BYTES);
+            tma_load_2d(&tmDy, &tail[s], sa, o, r);
+            tma_load_2d(&tmDy, &tail[s], sa + BOX, o + 64, r);
+            tma_load_2d(&tmX, &tail[s], sa + 2 * BOX, i, r);
+            tma_load_2d(&tmX, &tail[s], sa + 3 * BOX, i + 64, r);
+          } else {
+            const uint32_t fl = mapa(smem_u32(&full[s]), 0);
+            if (leader) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
+            else mbar_arrive_cluster(fl);
+            tma_load_2d_pair(&tmDy, fl, sa, o, r);
+            tma_load_2d_pair(&tmDy, fl, sa + BOX, o + 64, r);
+            tma_load_2d_pair(&tmX, fl, sa + 2 * BOX, i, r);
+            tma_load_2d_pair(&tmX, fl, sa + 3 * BOX, i + 64, r);
+          }
+        }
+      }
+      volatile int no_abort = 0;
+      for (int j = (it - S > 0 ? it - S : 0); j < it; ++j)
+        mbar_wait(&empty[j % S], (uint32_t)(j / S) & 1u, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------------ tail rows (both CTAs)
+    if (blockIdx.x == 0)
+      for (int g = lane; g < a.n; g += 32)
+        if (!group_ok(a.offsets[g], a.offsets[g + 1], a.n_rows)) set_status(MOE_ERR_DEVICE_CHECK);
+    int it = 0;
+    uint32_t uses = 0;       // parity of the uses of each stage's tail barrier
+    for (int tile = tile0; tile < total; tile += tstep) {
+      const Tile t = locate(tile);
+      if (idle(t)) continue;
+      it += t.nkb;
+      if (t.nkb == 0 || !is_tail(t, t.nkb - 1)) continue;
+      const int s = (it - 1) % S;
+      if (!mbar_wait(&tail[s], (uses >> s) & 1u, abort_flag)) break;
+      uses ^= 1u << s;
+      const int first = t.rows - (t.nkb - 1) * 64, end = (first + 15) & ~15;
+      uint8_t* sa = smem + (size_t)s * STAGE_BYTES;
+      // a row is one 128-byte line of each of the four boxes; the swizzle
+      // moves 16-byte pieces within a line only
+      for (int j = lane; j < (end - first) * 32; j += 32) {
+        const int row = first + (j >> 5), box = (j >> 3) & 3, piece = j & 7;
+        *reinterpret_cast<uint4*>(sa + box * BOX + row * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(&full[s]);
+        else mbar_arrive_cluster(mapa(smem_u32(&full[s]), 0));
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer (leader)
+    if (leader && elect_one()) {
+      int it = 0, tcount = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < total && ok; tile += tstep) {
+        const Tile t = locate(tile);
+        if (idle(t)) continue;
+        const uint32_t idesc = umma_idesc(1, TO, t.cols) | (1u << 15) | (1u << 16);
+        const int acc = tcount & 1;
+        const uint32_t use = (uint32_t)(tcount >> 1);
+        ++tcount;
+        if (!mbar_wait(&tempty[acc], (use & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
+        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+          const int s = it % S;
+          const uint32_t ph = (uint32_t)(it / S) & 1u;
+          if (!mbar_wait(&full[s], ph, abort_flag)) { ok = false; break; }
+          // the peer's cleared lines, released by its tail warp's arrival
+          if (is_tail(t, kb)) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + (size_t)s * STAGE_BYTES);
+          const uint64_t ad = gbwd::umma_desc_sw128_mn(sa);
+          const uint64_t bd = gbwd::umma_desc_sw128_mn(sa + 2 * BOX);
+          const int steps = min(4, (t.rows - kb * 64 + 15) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps)
+              umma_pair<0>(d_tmem, ad + (uint64_t)(128 * k), bd + (uint64_t)(128 * k), idesc,
+                           (kb | k) != 0 ? 1u : 0u);
+          const uint32_t e_local = smem_u32(&empty[s]);
+          umma_commit_pair(mapa(e_local, 0));
+          umma_commit_pair(mapa(e_local, 1));
+        }
+        if (ok) {
+          const uint32_t t_local = smem_u32(&tfull[acc]);
+          umma_commit_pair(mapa(t_local, 0));
+          umma_commit_pair(mapa(t_local, 1));
+        }
+      }
+      umma_commit_pair(mapa(smem_u32(drain), 0));
+      volatile int no_abort = 0;
+      mbar_wait(drain, 0, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ epilogue (both CTAs)
+    // 32 x 32 blocks through shared memory to TMA stores (or, accumulating,
+    // TMA additions: each element of dW is added to once), which clip the edges.
+    const int q = warp - 4;
+    uint8_t* stg = store_buf + (size_t)q * 2 * 4096;
+    const uint32_t tempty_leader0 = mapa(smem_u32(&tempty[0]), 0);
+    const uint32_t tempty_leader1 = mapa(smem_u32(&tempty[1]), 0);
+    int tcount = 0, nst = 0;
+    for (int tile = tile0; tile < total; tile += tstep) {
+      const Tile t = locate(tile);
+      if (idle(t)) continue;
+      const int acc = tcount & 1;
+      const uint32_t use = (uint32_t)(tcount >> 1);
+      ++tcount;
+      if (!mbar_wait(&tfull[acc], use & 1u, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+      const bool any = t.rows > 0;
+      const int o = t.ot * TO + (int)rank * 128 + q * 32;   // the warp's first output feature
+      const int chunks = o < a.d_out ? t.cols / 32 : 0;
+      for (int c = 0; c < chunks; ++c, ++nst) {
+        uint32_t va[16], vb[16];
+        tmem_ld16_nowait(tb + (uint32_t)(32 * c), va);
+        tmem_ld16_nowait(tb + (uint32_t)(32 * c + 16), vb);
+        tmem_wait_ld2(va, vb);
+        uint8_t* buf = stg + (size_t)(nst & 1) * 4096;
+        // the store issued from this buffer two chunks ago has read it
+        if (lane == 0) bulk_wait_group_read<1>();
+        __syncwarp();
+        if (OUT_BF16) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t* src = j < 2 ? &va[8 * j] : &vb[8 * (j - 2)];
+            uint32_t w4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w4[i] = any ? gemm::pack_bf16x2(__uint_as_float(src[2 * i]),
+                                              __uint_as_float(src[2 * i + 1]))
+                          : 0u;
+            *reinterpret_cast<uint4*>(buf + lane * 64 + j * 16) =
+                make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t* src = j < 4 ? &va[4 * j] : &vb[4 * (j - 4)];
+            const uint4 v = any ? make_uint4(src[0], src[1], src[2], src[3])
+                                : make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = v;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (a.accumulate) tma_add_3d(&tmC, buf, t.it * TI + 32 * c, o, t.g);
+          else gbwd::tma_store_3d(&tmC, buf, t.it * TI + 32 * c, o, t.g);
+          bulk_commit_group();
+        }
+      }
+      tc_fence_before();
+      if (leader) mbar_arrive(&tempty[acc]);
+      else mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
+    }
+    if (lane == 0) bulk_wait_group_all();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+}  // namespace grouped
+}  // namespace moe

@@ -1,0 +1,151 @@
+// Entry points of the grouped products.  Included by api.cu, whose helpers it
+// uses.
+#pragma once
+
+#include "grouped.cuh"
+
+namespace {
+
+// Tensor map of rank 2 or 3 over a contiguous array, 128-byte swizzle unless
+// `plain`; dims innermost first.
+moe_status grouped_map(CUtensorMap* m, const void* base, bool f32, int rank, const uint64_t* dims,
+                       const uint32_t* box, bool plain = false) {
+  const uint64_t esz = f32 ? 4 : 2;
+  cuuint64_t n[3], strides[2];
+  cuuint32_t b[3], one[3] = {1, 1, 1};
+  uint64_t bytes = esz;
+  for (int i = 0; i < rank; ++i) {
+    n[i] = dims[i] > 0 ? dims[i] : 1;
+    b[i] = box[i];
+    bytes *= n[i];
+    if (i + 1 < rank) strides[i] = bytes;
+  }
+  const CUresult r = g_encode(
+      m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+      (cuuint32_t)rank, const_cast<void*>(base), n, strides, b, one,
+      CU_TENSOR_MAP_INTERLEAVE_NONE, plain ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    snprintf(t_errmsg, sizeof(t_errmsg), "cuTensorMapEncodeTiled (grouped): CUresult %d (inner "
+             "%llu, rows %llu)", (int)r, (unsigned long long)n[0], (unsigned long long)n[1]);
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+moe_status grouped_dims(int32_t n_groups, int32_t n_rows, int32_t d_in, int32_t d_out) {
+  if (n_groups < 1 || n_groups > grouped::MAX_GROUPS || n_rows < 0 || d_in < 8 || d_out < 8 ||
+      d_in > 65536 || d_out > 65536 || d_in % 8 || d_out % 8)
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// y = rows x W^T (dx: rows x W); the weights [G, d_out, d_in]
+moe_status launch_grouped_mm(bool dx, int32_t G, int32_t R, int32_t d_in, int32_t d_out,
+                             const void* rows, const void* w, const int32_t* offsets, void* y,
+                             cudaStream_t st) {
+  const uint64_t contract = dx ? d_out : d_in, feats = dx ? d_in : d_out;
+  const uint64_t wdims[3] = {(uint64_t)d_in, (uint64_t)d_out, (uint64_t)G};
+  const uint32_t wbox[3] = {64, dx ? 64u : 128u, 1};
+  const uint64_t xdims[2] = {contract, (uint64_t)R};
+  const uint32_t xbox[2] = {64, 128}, sbox[2] = {64, grouped::SMALL_ROWS};
+  CUtensorMap tw, tx, ts;
+  moe_status rc = grouped_map(&tw, w, false, 3, wdims, wbox);
+  if (rc == MOE_OK) rc = grouped_map(&tx, rows, false, 2, xdims, xbox);
+  if (rc == MOE_OK) rc = grouped_map(&ts, rows, false, 2, xdims, sbox);
+  if (rc != MOE_OK) return rc;
+  grouped::Args a;
+  memset(&a, 0, sizeof(a));
+  a.offsets = offsets;
+  a.n = G;
+  a.n_rows = R;
+  a.feats = (int)feats;
+  a.contract = (int)contract;
+  a.y = static_cast<__nv_bfloat16*>(y);
+  // at most this many row tiles: every group may add a partly filled one
+  const int64_t row_tiles = R / 256 + (G < R ? G : R);
+  const int64_t tiles = row_tiles * (int64_t)((feats + 255) / 256);
+  auto* k = dx ? grouped::k_grouped_mm<true> : grouped::k_grouped_mm<false>;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  rc = pair_config(dx ? 5 : 4, k, grouped::MM_THREADS, grouped::MM_SMEM, tiles, st, &cfg, attr);
+  if (rc != MOE_OK) return rc;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, tw, tx, ts, a);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "k_grouped_mm");
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_grouped_mm(int32_t n_groups, int32_t n_rows, int32_t d_in, int32_t d_out,
+                          const void* x, const void* w, const int32_t* offsets, void* y,
+                          cudaStream_t stream) {
+  moe_status rc = grouped_dims(n_groups, n_rows, d_in, d_out);
+  if (rc != MOE_OK) return rc;
+  if (n_rows == 0) return MOE_OK;
+  if (!given(x) || !given(w) || !given(offsets) || !given(y) || y == x || y == w)
+    return MOE_ERR_INVALID_ARG;
+  int sms;
+  if ((rc = device_setup(&sms)) != MOE_OK) return rc;
+  return launch_grouped_mm(false, n_groups, n_rows, d_in, d_out, x, w, offsets, y, stream);
+}
+
+moe_status moe_grouped_mm_dx(int32_t n_groups, int32_t n_rows, int32_t d_in, int32_t d_out,
+                             const void* dy, const void* w, const int32_t* offsets, void* dx,
+                             cudaStream_t stream) {
+  moe_status rc = grouped_dims(n_groups, n_rows, d_in, d_out);
+  if (rc != MOE_OK) return rc;
+  if (n_rows == 0) return MOE_OK;
+  if (!given(dy) || !given(w) || !given(offsets) || !given(dx) || dx == dy || dx == w)
+    return MOE_ERR_INVALID_ARG;
+  int sms;
+  if ((rc = device_setup(&sms)) != MOE_OK) return rc;
+  return launch_grouped_mm(true, n_groups, n_rows, d_in, d_out, dy, w, offsets, dx, stream);
+}
+
+moe_status moe_grouped_mm_dw(int32_t n_groups, int32_t n_rows, int32_t d_in, int32_t d_out,
+                             const void* dy, const void* x, const int32_t* offsets, void* dw,
+                             int32_t bf16_grads, int32_t accumulate, cudaStream_t stream) {
+  moe_status rc = grouped_dims(n_groups, n_rows, d_in, d_out);
+  if (rc != MOE_OK) return rc;
+  if ((bf16_grads != 0 && bf16_grads != 1) || (accumulate != 0 && accumulate != 1) ||
+      (bf16_grads && accumulate))
+    return MOE_ERR_INVALID_ARG;
+  if (!given(offsets) || !given(dw) || (n_rows > 0 && (!given(dy) || !given(x))) || dw == dy ||
+      dw == x)
+    return MOE_ERR_INVALID_ARG;
+  if (n_rows == 0 && accumulate) return MOE_OK;
+  int sms;
+  if ((rc = device_setup(&sms)) != MOE_OK) return rc;
+  // without rows no group loads any: the maps only need some valid address
+  if (n_rows == 0) dy = x = dw;
+  const uint64_t ydims[2] = {(uint64_t)d_out, (uint64_t)n_rows};
+  const uint64_t xdims[2] = {(uint64_t)d_in, (uint64_t)n_rows};
+  const uint64_t cdims[3] = {(uint64_t)d_in, (uint64_t)d_out, (uint64_t)n_groups};
+  const uint32_t box[2] = {64, 64}, cbox[3] = {32, 32, 1};
+  CUtensorMap ty, tx, tc;
+  rc = grouped_map(&ty, dy, false, 2, ydims, box);
+  if (rc == MOE_OK) rc = grouped_map(&tx, x, false, 2, xdims, box);
+  if (rc == MOE_OK) rc = grouped_map(&tc, dw, !bf16_grads, 3, cdims, cbox, bf16_grads != 0);
+  if (rc != MOE_OK) return rc;
+  grouped::Args a;
+  memset(&a, 0, sizeof(a));
+  a.offsets = offsets;
+  a.n = n_groups;
+  a.n_rows = n_rows;
+  a.d_in = d_in;
+  a.d_out = d_out;
+  a.accumulate = accumulate;
+  const int64_t tiles = (int64_t)n_groups * ((d_in + 255) / 256) * ((d_out + 255) / 256);
+  auto* k = bf16_grads ? grouped::k_grouped_dw<true> : grouped::k_grouped_dw<false>;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  rc = pair_config(bf16_grads ? 7 : 6, k, grouped::DW_THREADS, grouped::DW_SMEM, tiles, stream,
+                   &cfg, attr);
+  if (rc != MOE_OK) return rc;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, ty, tx, tc, a);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "k_grouped_dw");
+}
+
+}  // extern "C"

@@ -552,6 +552,33 @@ moe_status moe_combine_norm_backward(const moe_norm_desc* desc, const void* y, c
                                      void* dgate, void* ws, size_t ws_bytes,
                                      cudaStream_t stream);
 
+/* ---- Products grouped by expert ----------------------------------------------
+ * One weight matrix per group applied to that group's rows of a ragged row
+ * list, for experts that are not the layer's SwiGLU (the rows and offsets are
+ * those of moe_permute): rows offsets[g] .. offsets[g+1]-1 belong to group g,
+ *   moe_grouped_mm     y_r  = W_g x_r
+ *   moe_grouped_mm_dx  dx_r = W_g^T dy_r
+ *   moe_grouped_mm_dw  dW_g = sum_r dy_r x_r^T
+ * bf16 operands, fp32 accumulation, each output rounded once.
+ *   x, dx [n_rows, d_in], y, dy [n_rows, d_out], w [n_groups, d_out, d_in] bf16
+ *   offsets [n_groups + 1] int32, non-decreasing, within [0, n_rows]; a group
+ *     that breaks this counts as empty and sets MOE_ERR_DEVICE_CHECK
+ *   dw [n_groups, d_out, d_in]: bf16 with bf16_grads 1, else fp32; groups
+ *     without rows get zeros.  accumulate 1 (fp32 only): added to dw instead,
+ *     groups without rows untouched.
+ * Rows of y and dx before offsets[0] and behind offsets[n_groups] are left as
+ * they were.  n_groups 1..1024, d_in and d_out multiples of 8 up to 65536.
+ * Outputs must not overlap inputs.  No workspace; one launch. */
+moe_status moe_grouped_mm(int32_t n_groups, int32_t n_rows, int32_t d_in, int32_t d_out,
+                          const void* x, const void* w, const int32_t* offsets, void* y,
+                          cudaStream_t stream);
+moe_status moe_grouped_mm_dx(int32_t n_groups, int32_t n_rows, int32_t d_in, int32_t d_out,
+                             const void* dy, const void* w, const int32_t* offsets, void* dx,
+                             cudaStream_t stream);
+moe_status moe_grouped_mm_dw(int32_t n_groups, int32_t n_rows, int32_t d_in, int32_t d_out,
+                             const void* dy, const void* x, const int32_t* offsets, void* dw,
+                             int32_t bf16_grads, int32_t accumulate, cudaStream_t stream);
+
 /* Human-readable name of a status. */
 const char* moe_status_string(moe_status status);
 

@@ -53,3 +53,29 @@ def combine_norm_backward(y, w, gate, gate_group, dh, eps):
         dgate = np.zeros_like(gate)
         np.add.at(dgate, np.arange(T) // gate_group, dh * w * n)
     return _through_norm(y, dh * g * w, eps), np.sum(dh * g * n, axis=0), dgate
+
+
+# ---------------------------------------------------------------- grouped products
+def _groups(offsets):
+    """(group, its rows); a group whose offsets decrease is empty."""
+    return [(g, slice(a, b)) for g, (a, b) in enumerate(zip(offsets[:-1], offsets[1:])) if b > a]
+
+
+def grouped_mm(x, w, offsets, y):
+    """y[r] = w[g] x[r]; rows of no group keep what y holds."""
+    y = y.copy()
+    for g, r in _groups(offsets):
+        y[r] = x[r] @ w[g].T
+    return y
+
+
+def grouped_mm_dx(dy, w, offsets, dx):
+    return grouped_mm(dy, w.transpose(0, 2, 1), offsets, dx)
+
+
+def grouped_mm_dw(dy, x, offsets, dw):
+    """dw[g] + sum_r dy[r] x[r]^T."""
+    dw = dw.copy()
+    for g, r in _groups(offsets):
+        dw[g] += dy[r].T @ x[r]
+    return dw

@@ -136,3 +136,66 @@ def test_norm_binding_refuses():
         with pytest.raises(moe.MoeError, match=what) as e:
             moe.moe_norm(d, *args)
         assert e.value.status == moe.ERR_INVALID_ARG
+
+
+# ---------------------------------------------------------------- grouped products
+def test_oracle_grouped_gradients_against_differences():
+    rng = np.random.default_rng(3)
+    offsets = np.array([1, 1, 4, 6])
+    x, w = rng.normal(size=(7, 3)), rng.normal(size=(3, 4, 3))
+    dy = rng.normal(size=(7, 4))
+
+    def loss():
+        return np.sum(dy * block.grouped_mm(x, w, offsets, np.zeros((7, 4))))
+
+    dx = block.grouped_mm_dx(dy, w, offsets, np.zeros_like(x))
+    dw = block.grouped_mm_dw(dy, x, offsets, np.zeros_like(w))
+    np.testing.assert_allclose(differences(loss, x), dx, atol=DIFF)
+    np.testing.assert_allclose(differences(loss, w), dw, atol=DIFF)
+
+
+def test_grouped_entry_points_reject_before_touching_cuda():
+    L, bad = moe.lib(), moe.ERR_INVALID_ARG
+    ok = (4, 16, 64, 128)
+    for dims in [(0, 16, 64, 128), (1025, 16, 64, 128), (4, -1, 64, 128), (4, 16, 0, 128),
+                 (4, 16, 68, 128), (4, 16, 64, 4), (4, 16, 64, 65544), (4, 16, 65544, 64)]:
+        assert L.moe_grouped_mm(*dims, 16, 32, 48, 64, None) == bad, dims
+        assert L.moe_grouped_mm_dx(*dims, 16, 32, 48, 64, None) == bad, dims
+        assert L.moe_grouped_mm_dw(*dims, 16, 32, 48, 64, 0, 0, None) == bad, dims
+    for i in range(4):
+        for wrong in (None, 40):
+            p = [16, 32, 48, 64]
+            p[i] = wrong
+            assert L.moe_grouped_mm(*ok, *p, None) == bad
+            assert L.moe_grouped_mm_dx(*ok, *p, None) == bad
+            assert L.moe_grouped_mm_dw(*ok, *p, 0, 0, None) == bad
+    for i in range(2):
+        p = [16, 32, 48, 64]
+        p[3] = p[i]
+        assert L.moe_grouped_mm(*ok, *p, None) == bad
+        assert L.moe_grouped_mm_dx(*ok, *p, None) == bad
+        assert L.moe_grouped_mm_dw(*ok, *p, 0, 0, None) == bad
+    for flags in [(2, 0), (0, 2), (-1, 0), (1, 1)]:
+        assert L.moe_grouped_mm_dw(*ok, 16, 32, 48, 64, *flags, None) == bad, flags
+    # nothing to do
+    assert L.moe_grouped_mm(4, 0, 64, 128, None, None, None, None, None) == moe.OK
+    assert L.moe_grouped_mm_dw(4, 0, 64, 128, None, None, 48, 64, 0, 1, None) == moe.OK
+
+
+def test_grouped_binding_refuses():
+    import torch
+    bf = dict(dtype=torch.bfloat16)
+    x, w, y = torch.zeros(9, 16, **bf), torch.zeros(2, 24, 16, **bf), torch.zeros(9, 24, **bf)
+    off = torch.zeros(3, dtype=torch.int32)
+    for args, what in [((x, w, off, y[:8]), "must be"), ((x, w[0], off, y), "n_groups"),
+                       ((x.float(), w, off, y), "float32"), ((x, w, off.long(), y), "int64"),
+                       ((x, w, off[:2], y), "holds"), ((x, w, off, y.t()), "must be"),
+                       ((x, w.transpose(1, 2), off, y), "must be|contiguous"),
+                       ((x, w, off, y), "CUDA")]:
+        with pytest.raises(moe.MoeError, match=what) as e:
+            moe.moe_grouped_mm(*args)
+        assert e.value.status == moe.ERR_INVALID_ARG
+    with pytest.raises(moe.MoeError, match="CUDA"):
+        moe.moe_grouped_mm_dx(y, w, off, x)
+    with pytest.raises(moe.MoeError, match="float16"):
+        moe.moe_grouped_mm_dw(y, x, off, w.half())
