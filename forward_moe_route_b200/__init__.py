@@ -60,6 +60,21 @@ class MoeNormDesc(ctypes.Structure):
                 ("eps", ctypes.c_float), ("res_scale", ctypes.c_float)]
 
 
+class MoeAdamwDesc(ctypes.Structure):
+    """moe_adamw_desc: hyperparameters of the AdamW step."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("seed", ctypes.c_uint64),
+                ("state_bits", ctypes.c_int32)]
+
+
+class MoeAdamwTensor(ctypes.Structure):
+    """moe_adamw_tensor: one tensor of the list."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("p", "grad", "m", "v", "m_scale", "v_scale",
+                                               "p_bf16")] + [
+                ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float),
+                ("grad_bf16", ctypes.c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -132,6 +147,11 @@ _SIGS = {
                                                  ctypes.c_size_t, _P]),
     "moe_grouped_mm": (ctypes.c_int, [ctypes.c_int32] * 4 + [_P] * 5),
     "moe_grouped_mm_dx": (ctypes.c_int, [ctypes.c_int32] * 4 + [_P] * 5),
+    "moe_adamw_table_size": (ctypes.c_size_t, [_P, ctypes.c_int32]),
+    "moe_adamw_table": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t,
+                                       ctypes.POINTER(ctypes.c_int64)]),
+    "moe_adamw": (ctypes.c_int, [ctypes.POINTER(MoeAdamwDesc), _P, ctypes.c_int32, ctypes.c_int64,
+                                 ctypes.c_int32, _P, _P, _P]),
     "moe_grouped_mm_dw": (ctypes.c_int, [ctypes.c_int32] * 4 + [_P] * 4 + [ctypes.c_int32] * 2 +
                           [_P]),
 }
@@ -838,3 +858,88 @@ def moe_grouped_mm_dw(dy, x, offsets, dw, accumulate: bool = False, stream=None)
     _check(_lib.moe_grouped_mm_dw(*dims, _ptr(dy), _ptr(x), _ptr(offsets), _ptr(dw),
                                   int(dw.element_size() == 2), int(accumulate),
                                   _stream(stream)), "moe_grouped_mm_dw")
+
+
+# ---- AdamW over a list of tensors ------------------------------------------------------------
+
+def make_adamw_desc(lr: float, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8,
+                    state_bits: int = 32, seed: int = 0) -> MoeAdamwDesc:
+    return MoeAdamwDesc(lr, beta1, beta2, eps, seed, state_bits)
+
+
+class AdamwTable:
+    """The device table of a tensor list, made by adamw_table; holds on to the tensors."""
+
+    def __init__(self, table, n_tensors: int, n_chunks: int, state_bits: int, tensors):
+        self.table, self.n_tensors, self.n_chunks = table, n_tensors, n_chunks
+        self.state_bits, self.tensors = state_bits, tensors
+
+
+_STATES = {32: ("float32",), 8: ("float8_e4m3fn", "uint8")}
+
+
+def adamw_table(p, grad, m, v, p_bf16=None, weight_decay=0.0, m_scale=None,
+                v_scale=None) -> AdamwTable:
+    """The table of the lists' tensors (equal lengths; p_bf16's items may be None): p fp32, grad
+    fp32 or bf16, m and v fp32, or E4M3 with m_scale and v_scale of one fp32 for 128 elements.
+    weight_decay: one number or one per tensor.  The tensors are updated in place by every
+    moe_adamw with this table and have to stay where they are."""
+    import torch
+    where = "adamw_table"
+    n = len(p)
+    bits = 32 if m_scale is None and v_scale is None else 8
+    none = [None] * n
+    decay = [weight_decay] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
+    lists = dict(p=p, grad=grad, m=m, v=v, p_bf16=none if p_bf16 is None else p_bf16,
+                 m_scale=none if bits == 32 else m_scale, v_scale=none if bits == 32 else v_scale,
+                 weight_decay=decay)
+    for name, items in lists.items():
+        if items is None or len(items) != n:
+            raise MoeError(ERR_INVALID_ARG, f"{where}: {name} is not a list of {n}")
+    array = (MoeAdamwTensor * n)()
+    held = []
+    for i in range(n):
+        t = {k: x[i] for k, x in lists.items()}
+        if t["p"] is None:
+            raise MoeError(ERR_INVALID_ARG, f"{where}: p[{i}] is missing")
+        size = t["p"].numel()
+        blocks = -(-size // 128)
+        for name, need, kinds in [("p", size, ("float32",)), ("grad", size, ("float32", "bfloat16")),
+                                  ("m", size, _STATES[bits]), ("v", size, _STATES[bits]),
+                                  ("m_scale", blocks, ("float32",)),
+                                  ("v_scale", blocks, ("float32",)),
+                                  ("p_bf16", size, ("bfloat16",))]:
+            _operand(where, f"{name}[{i}]", t[name], need, kinds,
+                     name == "p_bf16" or (bits == 32 and name.endswith("scale")))
+            if t[name] is not None and t[name].numel() != need:
+                raise MoeError(ERR_INVALID_ARG, f"{where}: {name}[{i}] holds {t[name].numel()} "
+                                                f"elements, not {need}")
+        tensors = [t[k] for k in ("p", "grad", "m", "v", "m_scale", "v_scale", "p_bf16")]
+        _on_device(where, [(f"tensor {i}", x) for x in tensors])
+        held.append(tensors)
+        array[i] = MoeAdamwTensor(*[None if x is None else x.data_ptr() for x in tensors], size,
+                                  t["weight_decay"], int(t["grad"].element_size() == 2))
+    bytes_ = int(_lib.moe_adamw_table_size(array, n))
+    if bytes_ == 0:
+        raise MoeError(ERR_INVALID_ARG, f"{where}: too many tensors or elements")
+    image = torch.empty(bytes_, dtype=torch.uint8)
+    chunks = ctypes.c_int64()
+    _check(_lib.moe_adamw_table(array, n, bits, image.data_ptr(), bytes_, ctypes.byref(chunks)),
+           where)
+    return AdamwTable(image.cuda(), n, chunks.value, bits, held)
+
+
+def moe_adamw(desc, table: AdamwTable, step, lr=None, stream=None) -> None:
+    """One AdamW step over the table's tensors.  step: an int >= 1, or a CUDA int32 tensor of one
+    element that the kernel reads; lr: None (desc.lr) or a CUDA float32 tensor of one element."""
+    if table.state_bits != desc.state_bits:
+        raise MoeError(ERR_INVALID_ARG, f"moe_adamw: a table of {table.state_bits}-bit states")
+    step_dev = None if isinstance(step, int) else step
+    if step_dev is not None:
+        _operand("moe_adamw", "step", step_dev, 1, ("int32",))
+    if lr is not None:
+        _operand("moe_adamw", "lr", lr, 1, ("float32",))
+    _on_device("moe_adamw", [("table", table.table), ("step", step_dev), ("lr", lr)])
+    _check(_lib.moe_adamw(ctypes.byref(desc), _ptr(table.table), table.n_tensors, table.n_chunks,
+                          step if step_dev is None else 0, _ptr(step_dev), _ptr(lr),
+                          _stream(stream)), "moe_adamw")

@@ -1,0 +1,316 @@
+// One AdamW step over a list of tensors in one launch.
+//
+//   m' = b1 m + (1 - b1) g,        v' = b2 v + (1 - b2) g^2
+//   p' = (1 - lr wd) p - lr / (1 - b1^t) m' / (sqrt(v' / (1 - b2^t)) + eps)
+//
+// in fp32 for every element of every tensor; p' is also rounded to bf16, and
+// m', v' are kept in fp32 or in 8 bits.
+//
+// 8-bit states.  128 elements in a row share a scale, max |x| / 448, and hold
+// x / scale as E4M3 codes; the second moment is held as its root, which halves
+// the range of exponents it has to cover.  Codes are rounded up with the
+// probability of the distance to the code below (the moments are averages over
+// many steps: increments below half a code step would be lost for good by
+// rounding to nearest).  A positive root never becomes code 0, so no element
+// whose gradient was ever seen divides by eps alone.  The random bits are a
+// counter-based generator's (Philox-2x32 with 7 rounds; Salmon et al.,
+// "Parallel random numbers: as easy as 1, 2, 3", SC 2011) keyed by seed and
+// step and counted by the element's place, so a step gives the same result
+// however it is split.
+//
+// Bound by memory: 24 to 28 bytes an element with fp32 states, 14 with 8-bit
+// ones.  A chunk of CHUNK elements of one tensor is a block's; a thread takes
+// 8 elements in a row: one 32-byte access for each fp32 operand, and the 16
+// lanes that share a scale find its maximum with four shuffles.  A table in
+// device memory, written once per list, names the tensor of each chunk.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+namespace adamw {
+
+constexpr int THREADS = 256;
+constexpr int PER = 8;                       // elements of a thread
+constexpr int CHUNK = THREADS * PER;
+constexpr int BLOCK = 128;                   // elements that share a scale
+constexpr int ROUNDS = 7;
+constexpr uint32_t KEY_STEP = 0x9E3779B9u;   // Philox key increment (Weyl)
+constexpr uint32_t PHILOX_M = 0xD256D193u;
+
+constexpr int GRAD_BF16 = 1;                 // Entry::flags
+constexpr int ALIGNED = 2;                   // every address fits the vector accesses
+constexpr int STATE8 = 4;
+
+struct alignas(16) Entry {
+  float* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  __nv_bfloat16* pb;
+  long long n;
+  int first;                                 // its first chunk
+  int flags;
+  float decay;
+  int spare;
+};
+
+// What a step adds to the hyperparameters.
+struct Coef {
+  float lr, alpha, root_mul;                 // lr / (1 - b1^t), (1 - b2^t)^-1/2
+  uint32_t key[ROUNDS];
+};
+
+struct Args {
+  const Entry* entries;
+  const int* tensor_of;                      // [chunks]
+  const int* step_dev;                       // read instead of coef when given
+  const float* lr_dev;
+  double lr, beta1, beta2;
+  float b1, b2, c1, c2, eps;                 // betas and 1 - betas
+  uint32_t seed;
+  int host_step;                             // without step_dev
+  Coef coef;
+};
+
+// b^t by squaring: t is at most 31 bits, and the relative error t 2^-53 is far
+// below the fp32 rounding of the result
+__host__ __device__ inline double power(double b, uint32_t t) {
+  double r = 1.0;
+  for (; t; t >>= 1, b *= b)
+    if (t & 1u) r *= b;
+  return r;
+}
+__host__ __device__ inline Coef coef_of(double lr, double beta1, double beta2, uint32_t seed,
+                                        uint32_t step) {
+  Coef c;
+  c.lr = (float)lr;
+  c.alpha = (float)(lr / (1.0 - power(beta1, step)));
+  c.root_mul = (float)(1.0 / sqrt(1.0 - power(beta2, step)));
+  uint32_t key = seed + step * KEY_STEP;
+  for (int r = 0; r < ROUNDS; ++r, key += KEY_STEP) c.key[r] = key;
+  return c;
+}
+
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// sqrt and reciprocal to within 2 units of 2^-23: next to the rounding of the
+// result they feed (p moves by lr times their quotient), nothing
+__device__ __forceinline__ float root_of(float x) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// E4M3 code of x, |x| <= 448 up to rounding, rounded up with the probability
+// of its distance from the code below; r: 16 random bits.  A NaN keeps its code.
+__device__ __forceinline__ uint32_t encode(float x, uint32_t r) {
+  const float a = fabsf(x);
+  // the 20 mantissa bits below E4M3's three decide against 16 random ones
+  int c = (int)((__float_as_uint(a) + (r << 4)) >> 20) - 960;
+  // below 2^-6 codes are multiples of 2^-9
+  if (a < 0.015625f) c = (int)floorf(fmaf(a, 512.0f, (float)r * 0x1p-16f));
+  c = min(c, 0x7e);
+  if (a != a) c = 0x7f;
+  return (uint32_t)c | (x < 0.f ? 0x80u : 0u);
+}
+
+__device__ __forceinline__ void decode4(uint32_t codes, float s, float* out) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const __half2_raw raw =
+        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes >> (16 * h)), __NV_E4M3);
+    const float2 f = __half22float2(__half2(raw));
+    out[2 * h] = f.x * s;
+    out[2 * h + 1] = f.y * s;
+  }
+}
+
+// max over the 16 lanes that share a scale; a NaN wins
+__device__ __forceinline__ float block_max(const float (&x)[8]) {
+  uint32_t most = 0;      // magnitudes order like their bits, NaN above infinity
+#pragma unroll
+  for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(x[j]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  return __uint_as_float(most);
+}
+
+template <bool STATES8>
+__global__ void __launch_bounds__(THREADS) k_adamw(const Args a) {
+  grid_dep_sync();
+  __shared__ Coef from_device;
+  const int t = a.tensor_of[blockIdx.x];
+  const Entry e = a.entries[t];
+  if (((e.flags & STATE8) != 0) != STATES8) {    // a table of the other kind
+    if (threadIdx.x == 0) set_status(MOE_ERR_DEVICE_CHECK);
+    return;
+  }
+  if (a.step_dev || a.lr_dev) {
+    const int step = a.step_dev ? *a.step_dev : a.host_step;
+    if (step < 1) {
+      if (threadIdx.x == 0) set_status(MOE_ERR_DEVICE_CHECK);
+      return;
+    }
+    if (threadIdx.x == 0)
+      from_device = coef_of(a.lr_dev ? (double)*a.lr_dev : a.lr, a.beta1, a.beta2, a.seed,
+                            (uint32_t)step);
+    __syncthreads();
+  }
+  const Coef& c = (a.step_dev || a.lr_dev) ? from_device : a.coef;
+  const long long at = (long long)((int)blockIdx.x - e.first) * CHUNK + threadIdx.x * PER;
+  const int here = (int)min((long long)PER, max(0ll, e.n - at));   // elements of this thread
+  const bool whole = (e.flags & ALIGNED) && here == PER;
+
+  float p[8], g[8], m[8], v[8];
+  if (whole) {
+    load8(e.p + at, p);
+    if (e.flags & GRAD_BF16) {
+      const uint4 raw = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(e.g) + at);
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        g[2 * j] = __uint_as_float(w[j] << 16);
+        g[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    } else {
+      load8(static_cast<const float*>(e.g) + at, g);
+    }
+    if (STATES8) {
+      const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(e.m) + at);
+      const uint2 cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(e.v) + at);
+      const float sm = e.m_scale[at / BLOCK], sv = e.v_scale[at / BLOCK];
+      decode4(cm.x, sm, m);
+      decode4(cm.y, sm, m + 4);
+      decode4(cv.x, sv, v);
+      decode4(cv.y, sv, v + 4);
+    } else {
+      load8(static_cast<const float*>(e.m) + at, m);
+      load8(static_cast<const float*>(e.v) + at, v);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      p[j] = g[j] = m[j] = v[j] = 0.f;
+      if (j >= here) continue;
+      p[j] = e.p[at + j];
+      g[j] = (e.flags & GRAD_BF16)
+                 ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.g)[at + j])
+                 : static_cast<const float*>(e.g)[at + j];
+      if (STATES8) {
+        float one[4];
+        decode4(static_cast<const uint8_t*>(e.m)[at + j], e.m_scale[at / BLOCK], one);
+        m[j] = one[0];
+        decode4(static_cast<const uint8_t*>(e.v)[at + j], e.v_scale[at / BLOCK], one);
+        v[j] = one[0];
+      } else {
+        m[j] = static_cast<const float*>(e.m)[at + j];
+        v[j] = static_cast<const float*>(e.v)[at + j];
+      }
+    }
+  }
+
+  const float keep = fmaf(-c.lr, e.decay, 1.0f);
+  float root[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (STATES8) v[j] *= v[j];
+    m[j] = fmaf(a.c1, g[j], a.b1 * m[j]);
+    v[j] = fmaf(a.c2, g[j] * g[j], a.b2 * v[j]);
+    root[j] = root_of(v[j]);
+    p[j] = fmaf(p[j], keep, -__fdividef(m[j] * c.alpha, fmaf(root[j], c.root_mul, a.eps)));
+  }
+
+  if (whole) {
+    store8(e.p + at, p);
+    if (e.pb) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(p[2 * j], p[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(e.pb + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < here) {
+        e.p[at + j] = p[j];
+        if (e.pb) e.pb[at + j] = __float2bfloat16_rn(p[j]);
+      }
+  }
+  if (!STATES8) {
+    if (whole) {
+      store8(static_cast<float*>(e.m) + at, m);
+      store8(static_cast<float*>(e.v) + at, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < here) {
+          static_cast<float*>(e.m)[at + j] = m[j];
+          static_cast<float*>(e.v)[at + j] = v[j];
+        }
+    }
+    return;
+  }
+
+  // scale and its inverse; a block below 2^-100 counts as zero (448 / max
+  // would leave fp32's range)
+  const float most_m = block_max(m), most_v = block_max(root);
+  const bool there_m = !(most_m < 0x1p-100f), there_v = !(most_v < 0x1p-100f);
+  const float inv_m = there_m ? 448.0f / most_m : 0.f, inv_v = there_v ? 448.0f / most_v : 0.f;
+  if ((threadIdx.x & 15) == 0 && here > 0) {
+    e.m_scale[at / BLOCK] = there_m ? most_m / 448.0f : 0.f;
+    e.v_scale[at / BLOCK] = there_v ? most_v / 448.0f : 0.f;
+  }
+  uint32_t cm[8], cv[8];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const unsigned long long pair = ((unsigned long long)at >> 1) + q;
+    uint32_t x = (uint32_t)pair, y = ((uint32_t)t << 8) ^ (uint32_t)(pair >> 32);
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+      const unsigned long long prod = (unsigned long long)x * PHILOX_M;
+      x = (uint32_t)(prod >> 32) ^ c.key[r] ^ y;
+      y = (uint32_t)prod;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = 2 * q + h;
+      const uint32_t word = h ? y : x;
+      cm[j] = encode(m[j] * inv_m, word & 0xffffu);
+      cv[j] = encode(root[j] * inv_v, word >> 16);
+      if (cv[j] == 0 && root[j] > 0.f) cv[j] = 1;
+    }
+  }
+  if (whole) {
+    auto pack = [](const uint32_t* b) {
+      return b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
+    };
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + at) = make_uint2(pack(cm), pack(cm + 4));
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + at) = make_uint2(pack(cv), pack(cv + 4));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < here) {
+        static_cast<uint8_t*>(e.m)[at + j] = (uint8_t)cm[j];
+        static_cast<uint8_t*>(e.v)[at + j] = (uint8_t)cv[j];
+      }
+  }
+}
+
+}  // namespace adamw
+}  // namespace moe

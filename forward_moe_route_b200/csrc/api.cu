@@ -2326,3 +2326,4 @@ moe_status moe_ipc_close(void* dev_ptr) {
 
 #include "norm_api.cuh"
 #include "grouped_api.cuh"
+#include "adamw_api.cuh"

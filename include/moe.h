@@ -579,6 +579,60 @@ moe_status moe_grouped_mm_dw(int32_t n_groups, int32_t n_rows, int32_t d_in, int
                              const void* dy, const void* x, const int32_t* offsets, void* dw,
                              int32_t bf16_grads, int32_t accumulate, cudaStream_t stream);
 
+/* ---- AdamW over a list of tensors ----------------------------------------------
+ * One launch updates every tensor of a list: fp32 master weights p from bf16 or
+ * fp32 gradients, with the moments in fp32 or in 8 bits, and (where given) the
+ * bf16 copy of p that the layer reads.  At step t = 1, 2, ...
+ *   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2
+ *   p = (1 - lr weight_decay) p - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
+ * in fp32.  8-bit moments: E4M3 codes with one fp32 scale, max / 448, for 128
+ * elements in a row (the last block of a tensor may be short); m as it is, v as
+ * its square root.  They are rounded at random, up with the probability of the
+ * distance; the same seed, step and list give the same codes.  Zeros start a
+ * list off (codes and scales 0).  A NaN or infinite gradient reaches p and the
+ * moments (a whole block of 8-bit ones). */
+typedef struct moe_adamw_desc {
+  double lr;           /* finite */
+  double beta1, beta2; /* in [0, 1) */
+  double eps;          /* > 0 in fp32 */
+  uint64_t seed;       /* of the 8-bit rounding */
+  int32_t state_bits;  /* 32 or 8 */
+} moe_adamw_desc;
+
+typedef struct moe_adamw_tensor {
+  float* p;              /* [n] */
+  const void* grad;      /* [n] bf16 with grad_bf16 1, else fp32 */
+  void* m;               /* [n] fp32 or E4M3 codes */
+  void* v;               /* [n] */
+  float* m_scale;        /* [ceil(n / 128)] (8-bit moments only) */
+  float* v_scale;
+  void* p_bf16;          /* [n] bf16 or NULL */
+  int64_t n;             /* elements, >= 0 */
+  float weight_decay;
+  int32_t grad_bf16;
+} moe_adamw_tensor;
+
+/* The table of a list, made once and used for every step: this fills a HOST
+ * buffer of moe_adamw_table_size(...) bytes, which the caller copies to a
+ * device buffer of the same size (the one table argument that is a host
+ * pointer; `tensors` is a host array of device pointers).  n_chunks: what
+ * moe_adamw takes.  Refused: memory that two tensors of the list, or two parts
+ * of one, would both write.  Addresses only need their element's alignment;
+ * tensors whose p, m, v (fp32) are 32-byte, grad 8-element, bf16 copy 16-byte
+ * and codes 8-byte aligned run fastest.  At most 2^24 tensors. */
+size_t moe_adamw_table_size(const moe_adamw_tensor* tensors, int32_t n_tensors);
+moe_status moe_adamw_table(const moe_adamw_tensor* tensors, int32_t n_tensors, int32_t state_bits,
+                           void* table, size_t table_bytes, int64_t* n_chunks);
+
+/* One step over the tensors of a device table.  step >= 1; with step_dev (one
+ * int32 on the device) that value is read when the kernel runs and `step` is
+ * ignored, and lr_dev (one fp32) replaces desc->lr the same way, so a captured
+ * graph follows both.  A step below 1 on the device, or a table made for the
+ * other state_bits, changes nothing and sets MOE_ERR_DEVICE_CHECK. */
+moe_status moe_adamw(const moe_adamw_desc* desc, const void* table, int32_t n_tensors,
+                     int64_t n_chunks, int32_t step, const int32_t* step_dev, const float* lr_dev,
+                     cudaStream_t stream);
+
 /* Human-readable name of a status. */
 const char* moe_status_string(moe_status status);
 

@@ -79,3 +79,55 @@ def grouped_mm_dw(dy, x, offsets, dw):
     for g, r in _groups(offsets):
         dw[g] += dy[r].T @ x[r]
     return dw
+
+
+# ---------------------------------------------------------------- AdamW
+SCALE_BLOCK = 128
+
+
+def adamw(p, g, m, v, step, lr, beta1, beta2, eps, decay):
+    """(p, m, v) after one step; fp64 arrays."""
+    m = beta1 * m + (1 - beta1) * g
+    v = beta2 * v + (1 - beta2) * g * g
+    root = np.sqrt(v / (1 - beta2 ** step))
+    return p - lr * (decay * p + m / (1 - beta1 ** step) / (root + eps)), m, v
+
+
+def block_scales(x):
+    """max |x| / 448 of every 128 elements, the last block short."""
+    pad = np.concatenate([x, np.zeros(-len(x) % SCALE_BLOCK)])
+    return np.abs(pad).reshape(-1, SCALE_BLOCK).max(1) / 448.0
+
+
+def spread(scales, n):
+    return np.repeat(scales, SCALE_BLOCK)[:n]
+
+
+def e4m3_value(codes):
+    """Values of E4M3 codes (uint8)."""
+    c = codes.astype(np.int64)
+    e, f = (c >> 3) & 15, c & 7
+    mag = np.where(e > 0, (8 + f) * 2.0 ** (e - 10), f * 2.0 ** -9)
+    mag = np.where((c & 0x7f) == 0x7f, np.nan, mag)
+    return np.where(c & 0x80, -mag, mag)
+
+
+def e4m3_position(a):
+    """Place of magnitudes 0 <= a <= 448 on the scale of the codes: a whole number at a code's
+    value, linear between two codes."""
+    e = np.maximum(np.floor(np.log2(np.maximum(a, 2.0 ** -40))), -6)
+    return np.where(a < 2.0 ** -6, a * 512, (e + 7) * 8 + (a / 2.0 ** e - 1) * 8)
+
+
+def random_words(n, tensor, seed, step):
+    """The generator's 32 bits for the n elements of tensor number `tensor` in the list."""
+    low = np.uint64(0xffffffff)
+    i = np.arange(n, dtype=np.uint64)
+    j = i >> np.uint64(1)
+    x, y = j & low, (np.uint64(tensor << 8) ^ (j >> np.uint64(32))) & low
+    key = ((seed ^ (seed >> 32)) + step * 0x9E3779B9) & 0xffffffff
+    for _ in range(7):
+        prod = x * np.uint64(0xD256D193)
+        x, y = (prod >> np.uint64(32)) ^ np.uint64(key) ^ y, prod & low
+        key = (key + 0x9E3779B9) & 0xffffffff
+    return np.where(i & np.uint64(1), y, x)

@@ -199,3 +199,115 @@ def test_grouped_binding_refuses():
         moe.moe_grouped_mm_dx(y, w, off, x)
     with pytest.raises(moe.MoeError, match="float16"):
         moe.moe_grouped_mm_dw(y, x, off, w.half())
+
+
+# ---------------------------------------------------------------- AdamW
+def test_oracle_codes_and_random_words():
+    import torch
+    codes = np.arange(256, dtype=np.uint8)
+    want = torch.from_numpy(codes).view(torch.float8_e4m3fn).double().numpy()
+    np.testing.assert_array_equal(block.e4m3_value(codes), want)
+    np.testing.assert_array_equal(block.e4m3_position(want[:0x7f]), np.arange(0x7f))
+    # the words are uniform and independent of one another: 2^16 of them, five standard deviations
+    w = np.concatenate([block.random_words(1 << 14, t, s, k)
+                        for t, s, k in ((0, 1, 1), (1, 1, 1), (0, 2, 1), (0, 1, 2))])
+    assert len(np.unique(w)) > len(w) - 8
+    for part in (w & 0xffff, w >> 16):
+        z = part / 65536 - 0.5
+        assert abs(z.mean()) < 5 / np.sqrt(12 * len(z))
+        assert abs(np.mean(z[:-1] * z[1:])) < 5 / 12 / np.sqrt(len(z))
+
+
+def adamw_entry(**kw):
+    base = dict(p=1 << 20, grad=2 << 20, m=3 << 20, v=4 << 20, m_scale=5 << 20, v_scale=6 << 20,
+                p_bf16=7 << 20, n=1000, weight_decay=0.1, grad_bf16=1)
+    base.update(kw)
+    return moe.MoeAdamwTensor(**base)
+
+
+def make_table(entries, bits=8, short=0):
+    L = moe.lib()
+    array = (moe.MoeAdamwTensor * max(1, len(entries)))(*entries)
+    size = L.moe_adamw_table_size(array, len(entries))
+    if size == 0:
+        return moe.ERR_INVALID_ARG, None, None
+    image = ctypes.create_string_buffer(size)
+    chunks = ctypes.c_int64(-1)
+    rc = L.moe_adamw_table(array, len(entries), bits, image, size - short, ctypes.byref(chunks))
+    return rc, chunks.value, image
+
+
+def test_adamw_table():
+    assert ctypes.sizeof(moe.MoeAdamwDesc) == 48 and ctypes.sizeof(moe.MoeAdamwTensor) == 72
+    rc, chunks, _ = make_table([adamw_entry()])
+    assert rc == moe.OK and chunks == 1
+    rc, chunks, _ = make_table([])
+    assert rc == moe.OK and chunks == 0
+    far = {k: v + (64 << 20) for k, v in
+           dict(p=1 << 20, grad=2 << 20, m=3 << 20, v=4 << 20, m_scale=5 << 20, v_scale=6 << 20,
+                p_bf16=7 << 20).items()}
+    rc, chunks, _ = make_table([adamw_entry(n=2048), adamw_entry(n=0, p=None),
+                                adamw_entry(n=2049, **far)])
+    assert rc == moe.OK and chunks == 3
+    # two tensors may share a gradient, not what is written
+    rc, chunks, _ = make_table([adamw_entry(), adamw_entry(**{**far, "grad": 2 << 20})])
+    assert rc == moe.OK
+    for k in ("p", "m", "v", "m_scale", "v_scale", "p_bf16"):
+        kw = {**far, k: getattr(adamw_entry(), k)}
+        assert make_table([adamw_entry(), adamw_entry(**kw)])[0] == moe.ERR_INVALID_ARG, k
+        assert make_table([adamw_entry(grad=getattr(adamw_entry(), k))])[0] == moe.ERR_INVALID_ARG
+    # the last element of one in the first of the next
+    assert make_table([adamw_entry(), adamw_entry(**{**far, "p": (1 << 20) + 3996})])[0] != moe.OK
+    assert make_table([adamw_entry(), adamw_entry(**{**far, "p": (1 << 20) + 4000})])[0] == moe.OK
+
+
+@pytest.mark.parametrize("kw", [dict(p=None), dict(grad=None), dict(m=None), dict(v=None),
+                                dict(m_scale=None), dict(v_scale=None), dict(n=-1),
+                                dict(n=1 << 43), dict(grad_bf16=2), dict(p=(1 << 20) + 2),
+                                dict(grad=(2 << 20) + 1), dict(p_bf16=(7 << 20) + 1),
+                                dict(m_scale=(5 << 20) + 2),
+                                dict(weight_decay=float("nan"))])
+def test_adamw_table_refuses(kw):
+    assert make_table([adamw_entry(**kw)])[0] == moe.ERR_INVALID_ARG
+    if "scale" not in str(kw):
+        assert make_table([adamw_entry(**kw)], bits=32)[0] == moe.ERR_INVALID_ARG
+
+
+def test_adamw_refuses():
+    L, bad = moe.lib(), moe.ERR_INVALID_ARG
+    assert make_table([adamw_entry()], bits=16)[0] == bad
+    assert make_table([adamw_entry()], short=1)[0] == moe.ERR_WORKSPACE
+    d = moe.make_adamw_desc(1e-3)
+    r = ctypes.byref(d)
+    assert L.moe_adamw(r, None, 0, 0, 1, None, None, None) == moe.OK
+    assert L.moe_adamw(None, 16, 1, 1, 1, None, None, None) == bad
+    for args in [(16, 1, 1, 0, None, None), (16, 1, 1, -3, None, None), (None, 1, 1, 1, None, None),
+                 (24, 1, 1, 1, None, None), (16, 0, 1, 1, None, None), (16, -1, 1, 1, None, None),
+                 (16, 1, -1, 1, None, None), (16, 1, 1, 0, 2, None), (16, 1, 1, 1, None, 6),
+                 (16, 1, 1 << 31, 1, None, None)]:
+        assert L.moe_adamw(r, *args, None) == bad, args
+    for kw in [dict(lr=float("nan")), dict(lr=float("inf")), dict(beta1=1.0), dict(beta1=-0.1),
+               dict(beta2=1.0), dict(beta2=float("nan")), dict(eps=0.0), dict(eps=1e-60),
+               dict(eps=float("inf")), dict(state_bits=16)]:
+        x = moe.make_adamw_desc(**{"lr": 1e-3, **kw})
+        assert L.moe_adamw(ctypes.byref(x), 16, 1, 1, 1, None, None, None) == bad, kw
+
+
+def test_adamw_binding_refuses():
+    import torch
+    f = torch.zeros(256)
+    e = torch.zeros(256, dtype=torch.uint8)
+    s = torch.zeros(2)
+    for kw, what in [(dict(grad=[f.double()]), "float64"), (dict(m=[e]), "uint8"),
+                     (dict(v=[f[:200]]), "holds"), (dict(p=[f[::2]]), "contiguous"),
+                     (dict(p_bf16=[f]), "float32"), (dict(m=[f, f]), "not a list"),
+                     (dict(m_scale=[s]), "v_scale is not"), (dict(p=[None]), "missing"),
+                     (dict(weight_decay=[0.1, 0.2]), "weight_decay is not"),
+                     (dict(m_scale=[s], v_scale=[s]), "float32, not"),
+                     (dict(m=[e], v=[e], m_scale=[s[:1]], v_scale=[s]), "holds"),
+                     (dict(), "CUDA")]:
+        with pytest.raises(moe.MoeError, match=what) as err:
+            moe.adamw_table(**{**dict(p=[f], grad=[f], m=[f], v=[f]), **kw})
+        assert err.value.status == moe.ERR_INVALID_ARG
+    with pytest.raises(moe.MoeError, match="8-bit"):
+        moe.moe_adamw(moe.make_adamw_desc(1e-3), moe.AdamwTable(None, 0, 0, 8, []), 1)
