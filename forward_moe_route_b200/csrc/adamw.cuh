@@ -106,25 +106,62 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
                : "memory");
 }
 
-// sqrt and reciprocal to within 2 units of 2^-23: next to the rounding of the
-// result they feed (p moves by lr times their quotient), nothing
+// sqrt(x) and 1 / x to within 2^-23 (x > 0 and normal for the inverse, 0 beyond
+// 2^126): next to the rounding of the p that they move by lr at most, nothing
 __device__ __forceinline__ float root_of(float x) {
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float inverse(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
-// E4M3 code of x, |x| <= 448 up to rounding, rounded up with the probability
-// of its distance from the code below; r: 16 random bits.  A NaN keeps its code.
-__device__ __forceinline__ uint32_t encode(float x, uint32_t r) {
-  const float a = fabsf(x);
-  // the 20 mantissa bits below E4M3's three decide against 16 random ones
-  int c = (int)((__float_as_uint(a) + (r << 4)) >> 20) - 960;
-  // below 2^-6 codes are multiples of 2^-9
-  if (a < 0.015625f) c = (int)floorf(fmaf(a, 512.0f, (float)r * 0x1p-16f));
-  c = min(c, 0x7e);
-  if (a != a) c = 0x7f;
-  return (uint32_t)c | (x < 0.f ? 0x80u : 0u);
+// E4M3 code of |x| <= 448 (up to rounding) in the top byte, rounded up with the
+// probability of its distance from the code below; r: 16 random bits, shifted
+// left by 4.  The 20 mantissa bits below E4M3's three decide against them: a
+// carry makes the next code.  Only for |x| >= 2^-6.
+__device__ __forceinline__ uint32_t encode_top(float x, uint32_t r4) {
+  const uint32_t c = (__float_as_uint(x) & 0x7fffffffu) - (960u << 20) + r4;
+  return (min(c, 0x07efffffu) << 4) | (__float_as_uint(x) & 0x80000000u);
+}
+// the same below 2^-6, where codes are multiples of 2^-9
+__device__ __forceinline__ uint32_t encode_small_top(float x, uint32_t r4) {
+  const uint32_t c = (uint32_t)fmaf(fabsf(x), 512.0f, (float)r4 * 0x1p-20f);
+  return (c << 24) | (__float_as_uint(x) & 0x80000000u);
+}
+
+// 8 codes of x * inv; r4(j): the random bits of element j.  NONZERO: a positive
+// x is not held as 0.
+template <bool NONZERO, typename R>
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv, float most, R r4) {
+  uint32_t c[8];
+  float y[8], least = 1.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    y[j] = x[j] * inv;
+    c[j] = encode_top(y[j], r4(j));
+    least = fminf(least, fabsf(y[j]));
+  }
+  if (least < 0.015625f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (fabsf(y[j]) < 0.015625f) {
+        c[j] = encode_small_top(y[j], r4(j));
+        if (NONZERO && x[j] > 0.f) c[j] = max(c[j], 1u << 24);
+      }
+  }
+  // an infinity or a NaN leaves its block without a scale: NaN codes
+  if (!(most <= 3.402823466e38f)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = 0x7f000000u;
+  }
+  auto top4 = [](const uint32_t* b) {
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0073), __byte_perm(b[2], b[3], 0x0073), 0x5410);
+  };
+  return make_uint2(top4(c), top4(c + 4));
 }
 
 __device__ __forceinline__ void decode4(uint32_t codes, float s, float* out) {
@@ -148,7 +185,7 @@ __device__ __forceinline__ float block_max(const float (&x)[8]) {
   return __uint_as_float(most);
 }
 
-template <bool STATES8>
+template <bool STATES8, bool FROM_DEVICE>
 __global__ void __launch_bounds__(THREADS) k_adamw(const Args a) {
   grid_dep_sync();
   __shared__ Coef from_device;
@@ -158,7 +195,7 @@ __global__ void __launch_bounds__(THREADS) k_adamw(const Args a) {
     if (threadIdx.x == 0) set_status(MOE_ERR_DEVICE_CHECK);
     return;
   }
-  if (a.step_dev || a.lr_dev) {
+  if (FROM_DEVICE) {
     const int step = a.step_dev ? *a.step_dev : a.host_step;
     if (step < 1) {
       if (threadIdx.x == 0) set_status(MOE_ERR_DEVICE_CHECK);
@@ -169,7 +206,7 @@ __global__ void __launch_bounds__(THREADS) k_adamw(const Args a) {
                             (uint32_t)step);
     __syncthreads();
   }
-  const Coef& c = (a.step_dev || a.lr_dev) ? from_device : a.coef;
+  const Coef& c = FROM_DEVICE ? from_device : a.coef;
   const long long at = (long long)((int)blockIdx.x - e.first) * CHUNK + threadIdx.x * PER;
   const int here = (int)min((long long)PER, max(0ll, e.n - at));   // elements of this thread
   const bool whole = (e.flags & ALIGNED) && here == PER;
@@ -226,11 +263,19 @@ __global__ void __launch_bounds__(THREADS) k_adamw(const Args a) {
   float root[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (STATES8) v[j] *= v[j];
-    m[j] = fmaf(a.c1, g[j], a.b1 * m[j]);
-    v[j] = fmaf(a.c2, g[j] * g[j], a.b2 * v[j]);
-    root[j] = root_of(v[j]);
-    p[j] = fmaf(p[j], keep, -__fdividef(m[j] * c.alpha, fmaf(root[j], c.root_mul, a.eps)));
+    if (STATES8) {
+      // each operation of the formulas rounded by itself: the codes are drawn
+      // from these values, and a last bit that differs can change a code
+      v[j] = __fmul_rn(v[j], v[j]);
+      m[j] = __fadd_rn(__fmul_rn(a.b1, m[j]), __fmul_rn(a.c1, g[j]));
+      v[j] = __fadd_rn(__fmul_rn(a.b2, v[j]), __fmul_rn(a.c2, __fmul_rn(g[j], g[j])));
+      root[j] = __fsqrt_rn(v[j]);
+    } else {
+      m[j] = fmaf(a.c1, g[j], a.b1 * m[j]);
+      v[j] = fmaf(a.c2, g[j] * g[j], a.b2 * v[j]);
+      root[j] = root_of(v[j]);
+    }
+    p[j] = fmaf(p[j], keep, -(m[j] * c.alpha) * inverse(fmaf(root[j], c.root_mul, a.eps)));
   }
 
   if (whole) {
@@ -271,12 +316,13 @@ __global__ void __launch_bounds__(THREADS) k_adamw(const Args a) {
   // would leave fp32's range)
   const float most_m = block_max(m), most_v = block_max(root);
   const bool there_m = !(most_m < 0x1p-100f), there_v = !(most_v < 0x1p-100f);
-  const float inv_m = there_m ? 448.0f / most_m : 0.f, inv_v = there_v ? 448.0f / most_v : 0.f;
+  const float inv_m = there_m ? __frcp_rn(most_m) * 448.0f : 0.f;
+  const float inv_v = there_v ? __frcp_rn(most_v) * 448.0f : 0.f;
   if ((threadIdx.x & 15) == 0 && here > 0) {
-    e.m_scale[at / BLOCK] = there_m ? most_m / 448.0f : 0.f;
-    e.v_scale[at / BLOCK] = there_v ? most_v / 448.0f : 0.f;
+    e.m_scale[at / BLOCK] = there_m ? most_m * (1.0f / 448.0f) : 0.f;
+    e.v_scale[at / BLOCK] = there_v ? most_v * (1.0f / 448.0f) : 0.f;
   }
-  uint32_t cm[8], cv[8];
+  uint32_t word[8];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const unsigned long long pair = ((unsigned long long)at >> 1) + q;
@@ -287,27 +333,22 @@ __global__ void __launch_bounds__(THREADS) k_adamw(const Args a) {
       x = (uint32_t)(prod >> 32) ^ c.key[r] ^ y;
       y = (uint32_t)prod;
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = 2 * q + h;
-      const uint32_t word = h ? y : x;
-      cm[j] = encode(m[j] * inv_m, word & 0xffffu);
-      cv[j] = encode(root[j] * inv_v, word >> 16);
-      if (cv[j] == 0 && root[j] > 0.f) cv[j] = 1;
-    }
+    word[2 * q] = x;
+    word[2 * q + 1] = y;
   }
+  const uint2 cm = encode8<false>(m, inv_m, most_m,
+                                  [&](int j) { return (word[j] << 4) & 0xffff0u; });
+  const uint2 cv = encode8<true>(root, inv_v, most_v,
+                                 [&](int j) { return (word[j] >> 12) & 0xffff0u; });
   if (whole) {
-    auto pack = [](const uint32_t* b) {
-      return b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
-    };
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + at) = make_uint2(pack(cm), pack(cm + 4));
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + at) = make_uint2(pack(cv), pack(cv + 4));
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + at) = cm;
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + at) = cv;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j < here) {
-        static_cast<uint8_t*>(e.m)[at + j] = (uint8_t)cm[j];
-        static_cast<uint8_t*>(e.v)[at + j] = (uint8_t)cv[j];
+        static_cast<uint8_t*>(e.m)[at + j] = (uint8_t)((j < 4 ? cm.x : cm.y) >> (8 * (j & 3)));
+        static_cast<uint8_t*>(e.v)[at + j] = (uint8_t)((j < 4 ? cv.x : cv.y) >> (8 * (j & 3)));
       }
   }
 }

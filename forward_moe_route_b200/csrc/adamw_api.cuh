@@ -2,6 +2,8 @@
 // Included by api.cu, whose helpers it uses.
 #pragma once
 
+#include <float.h>
+
 #include <algorithm>
 #include <cmath>
 #include <vector>
@@ -124,7 +126,7 @@ moe_status moe_adamw(const moe_adamw_desc* desc, const void* table, int32_t n_te
                      cudaStream_t stream) {
   if (!desc || (desc->state_bits != 8 && desc->state_bits != 32) || !std::isfinite(desc->lr) ||
       !(desc->beta1 >= 0.0 && desc->beta1 < 1.0) || !(desc->beta2 >= 0.0 && desc->beta2 < 1.0) ||
-      !std::isfinite(desc->eps) || !((float)desc->eps > 0.f))
+      !std::isfinite((float)desc->eps) || !((float)desc->eps >= FLT_MIN))
     return MOE_ERR_INVALID_ARG;
   if (n_tensors < 0 || n_tensors > kMaxTensors || n_chunks < 0 || n_chunks > kMaxChunks ||
       (!step_dev && step < 1) || ((uintptr_t)step_dev & 3) || ((uintptr_t)lr_dev & 3))
@@ -151,10 +153,12 @@ moe_status moe_adamw(const moe_adamw_desc* desc, const void* table, int32_t n_te
   a.eps = (float)desc->eps;
   a.seed = (uint32_t)(desc->seed ^ (desc->seed >> 32));
   a.host_step = step_dev ? 0 : step;
-  if (!step_dev && !lr_dev) a.coef = adamw::coef_of(a.lr, a.beta1, a.beta2, a.seed, (uint32_t)step);
-  return launch_chain("k_adamw", desc->state_bits == 8 ? adamw::k_adamw<true>
-                                                       : adamw::k_adamw<false>,
-                      dim3((unsigned)n_chunks), dim3(adamw::THREADS), 0, stream, a);
+  const bool dev = step_dev || lr_dev;
+  if (!dev) a.coef = adamw::coef_of(a.lr, a.beta1, a.beta2, a.seed, (uint32_t)step);
+  auto* k = desc->state_bits == 8
+                ? (dev ? adamw::k_adamw<true, true> : adamw::k_adamw<true, false>)
+                : (dev ? adamw::k_adamw<false, true> : adamw::k_adamw<false, false>);
+  return launch_chain("k_adamw", k, dim3((unsigned)n_chunks), dim3(adamw::THREADS), 0, stream, a);
 }
 
 }  // extern "C"

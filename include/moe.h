@@ -594,7 +594,7 @@ moe_status moe_grouped_mm_dw(int32_t n_groups, int32_t n_rows, int32_t d_in, int
 typedef struct moe_adamw_desc {
   double lr;           /* finite */
   double beta1, beta2; /* in [0, 1) */
-  double eps;          /* > 0 in fp32 */
+  double eps;          /* in fp32 at least FLT_MIN, finite */
   uint64_t seed;       /* of the 8-bit rounding */
   int32_t state_bits;  /* 32 or 8 */
 } moe_adamw_desc;
