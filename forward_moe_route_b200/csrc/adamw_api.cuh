@@ -15,7 +15,10 @@ namespace {
 constexpr int kMaxTensors = 1 << 24;    // the random counter has 24 bits for the tensor
 constexpr int64_t kMaxChunks = 0x7fffffff;
 
-int64_t adamw_chunks(int64_t n) { return n / adamw::CHUNK + (n % adamw::CHUNK != 0); }
+int64_t adamw_chunks(int64_t n, bool small) {
+  const int64_t size = small ? adamw::CHUNK8 : adamw::CHUNK;
+  return n / size + (n % size != 0);
+}
 
 // total chunks of the list, -1 when a length or the count is not accepted
 int64_t adamw_list_chunks(const moe_adamw_tensor* tensors, int32_t n) {
@@ -23,7 +26,7 @@ int64_t adamw_list_chunks(const moe_adamw_tensor* tensors, int32_t n) {
   int64_t chunks = 0;
   for (int32_t i = 0; i < n; ++i) {
     if (tensors[i].n < 0) return -1;
-    const int64_t c = adamw_chunks(tensors[i].n);
+    const int64_t c = adamw_chunks(tensors[i].n, false);   // the larger count of the two
     if (c > kMaxChunks - chunks) return -1;
     chunks += c;
   }
@@ -107,7 +110,7 @@ moe_status moe_adamw_table(const moe_adamw_tensor* tensors, int32_t n_tensors, i
     e.first = (int)chunk;
     e.decay = s.weight_decay;
     memcpy(image + (size_t)i * sizeof(e), &e, sizeof(e));
-    for (int64_t c = adamw_chunks(s.n); c > 0; --c) map[chunk++] = i;
+    for (int64_t c = adamw_chunks(s.n, small); c > 0; --c) map[chunk++] = i;
   }
   // nothing that is written may be any other tensor's, or another part of the same
   std::sort(spans.begin(), spans.end());
