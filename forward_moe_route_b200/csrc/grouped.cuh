@@ -22,14 +22,17 @@
 // group's last stage only the 16-row steps that hold rows are issued, and in
 // the last step the shared-memory lines behind the group's end are overwritten
 // with zeros in both operands: that stage's copies complete on a barrier of
-// their own in each CTA (one per stage), warp 3 clears the lines (fewer than 16) and then
-// arrives for the stage in the producer's place.  No row is copied or padded in
-// global memory.
+// their own in each CTA (one per stage), warp 3 clears the lines (fewer than 16)
+// and the leader's, when the peer's has reported too, arrives for the stage in
+// the producer's place.  (Having the peer's producer or tail warp arrive on the
+// leader's barrier for every stage cost a remote arrival a stage: 631 us instead
+// of 337 us at 16 groups of 1024 rows, 2048 x 7168.)  No row is copied or padded
+// in global memory.
 //
 // Every CTA reads the offsets itself (no preparing launch); a group whose offsets decrease or leave [0, n_rows] is reported and
 // treated as empty.
 //
-// Warp roles (384 threads in k_grouped_mm, 256 in k_grouped_dw): warp 0 TMA
+// Warp roles (384 threads): warp 0 TMA
 // producer, warp 1 MMA issuer (leader CTA), warp 2 TMEM allocator, warp 3 tail
 // rows (k_grouped_dw), the rest epilogue.  Two accumulators of 256 columns.
 // Barriers and bounded waits as in gemm_t.cuh.
@@ -45,14 +48,13 @@ namespace moe {
 namespace grouped {
 
 constexpr int MAX_GROUPS = 1024;
-constexpr int STAGES = 6;
+constexpr int STAGES = 6;                      // k_grouped_mm; DW_STAGES in k_grouped_dw
 constexpr uint32_t STAGE_BYTES = 32768;        // 16 KB of either operand per CTA
 constexpr uint32_t HALF_STAGE = STAGE_BYTES / 2;
-constexpr int SMALL_ROWS = 32;                 // rows of the small row box
 constexpr int ACC_COLS = 256;
 constexpr int TMEM_COLS = 512;
-constexpr uint32_t BAR_BYTES = (3 * STAGES + 6) * 8 + 16;
-constexpr uint32_t TAB_BYTES = (3 * MAX_GROUPS + 1) * 4 + 12;
+constexpr uint32_t BAR_BYTES = (4 * STAGES + 6) * 8 + 16;
+constexpr uint32_t TAB_BYTES = (3 * MAX_GROUPS + 1) * 4 + MAX_GROUPS * 2 + 12;
 
 // ---- rows on the N side -------------------------------------------------------------
 constexpr int MM_THREADS = 384;
@@ -62,9 +64,15 @@ constexpr uint32_t MM_SMEM = 1024 + STAGES * STAGE_BYTES + MM_EPI_WARPS * MM_XPO
                              TAB_BYTES;
 
 // ---- weight gradients -----------------------------------------------------------------
-constexpr int DW_THREADS = 256;
-constexpr uint32_t DW_STORE = 4 * 2 * 4096;
-constexpr uint32_t DW_SMEM = 1024 + STAGES * STAGE_BYTES + DW_STORE + BAR_BYTES;
+constexpr int DW_THREADS = 384;
+constexpr int DW_EPI_WARPS = 8;
+constexpr int DW_STAGES = 5;
+// a warp's staging: two blocks of 32 rows of 128 bytes
+constexpr uint32_t DW_STAGING = 8192;
+constexpr uint32_t DW_STORE = DW_EPI_WARPS * DW_STAGING;
+constexpr int DW_SORTED = 512;                 // most groups taken in order of their rows
+constexpr uint32_t DW_SMEM = 1024 + DW_STAGES * STAGE_BYTES + DW_STORE + BAR_BYTES +
+                             DW_SORTED * 2;
 static_assert(MM_SMEM <= 232448 && DW_SMEM <= 232448, "shared memory of one block");
 
 struct Args {
@@ -98,39 +106,103 @@ __device__ __forceinline__ bool group_ok(int r0, int r1, int n_rows) {
   return r0 >= 0 && r1 >= r0 && r1 <= n_rows;
 }
 
-// The group list in shared memory: first row and rows of each group, and the
-// prefix of its row tiles.  One warp builds it.
-struct Groups {
-  int *row0, *rows, *prefix;   // [n], [n], [n + 1]
-  int n;
-  __device__ __forceinline__ Groups(int* base, int count)
-      : row0(base), rows(base + MAX_GROUPS), prefix(base + 2 * MAX_GROUPS), n(count) {}
-  __device__ __forceinline__ void build(const int* offsets, int n_rows, int tile_rows) {
-    const int lane = lane_id();
-    int carry = 0;
+// Stable counting sort of n groups by key(g) in [0, KEYS), by one warp with
+// `slot` [KEYS] in shared memory: put(place, g) is called once for each group,
+// lower keys first, equal keys in the groups' order, so that every block comes
+// to the same list.
+template <int KEYS, typename Key, typename Put>
+__device__ __forceinline__ void warp_sort(int* slot, int n, Key key, Put put) {
+  static_assert(KEYS % 32 == 0, "");
+  const int lane = lane_id();
+  for (int k = lane; k < KEYS; k += 32) slot[k] = 0;
+  __syncwarp();
+  // visit(g, k, place) with the place among equal keys, slot[k] moved on
+  auto sweep = [&](auto visit) {
     for (int base = 0; base < n; base += 32) {
       const int g = base + lane;
-      int r0 = 0, r = 0;
-      if (g < n) {
-        r0 = offsets[g];
-        const int r1 = offsets[g + 1];
-        if (!group_ok(r0, r1, n_rows)) {
-          set_status(MOE_ERR_DEVICE_CHECK);
-          r0 = 0;
-        } else {
-          r = r1 - r0;
-        }
-        row0[g] = r0;
-        rows[g] = r;
+      const int k = g < n ? key(g) : -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, k);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      const int from = k >= 0 ? slot[k] : 0;
+      __syncwarp();
+      if (k >= 0) {
+        if (rank == 0) slot[k] = from + __popc(same);
+        visit(g, from + rank);
       }
-      const int v = (r + tile_rows - 1) / tile_rows;
+      __syncwarp();
+    }
+  };
+  sweep([](int, int) {});
+  int carry = 0;
+  for (int base = 0; base < KEYS; base += 32) {
+    const int count = slot[base + lane];
+    int incl = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    slot[base + lane] = carry + incl - count;
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  __syncwarp();
+  sweep([&](int g, int place) { put(place, g); });
+}
+
+// Tiles of a pair: wave after wave over all pairs, every other wave backwards.
+// The tiles come in order of falling cost, so the pairs' sums differ by less
+// than one tile whatever the groups' loads.
+__device__ __forceinline__ int tile_of(int wave) {
+  const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+  return wave * pairs + ((wave & 1) ? pairs - 1 - pair : pair);
+}
+
+// k_grouped_mm cuts a group of r rows into ceil(r / 256) row tiles of equal
+// height, rounded up to the 32 rows that the UMMA N goes by (r = 257: 160 + 97,
+// not 256 + 1).
+constexpr int TILE_ROWS = 256;
+__device__ __forceinline__ int row_tiles(int rows) { return (rows + TILE_ROWS - 1) / TILE_ROWS; }
+__device__ __forceinline__ int tile_height(int rows) {
+  const int n = row_tiles(rows);
+  return n ? ((rows + n - 1) / n + 31) & ~31 : 0;
+}
+
+// The group list in shared memory, in order of falling tile height: first row,
+// rows and number of each group, and the prefix of the row tiles.  One warp
+// builds it.
+struct Groups {
+  int *row0, *rows, *prefix;   // [n], [n], [n + 1]
+  uint16_t* id;                // [n]
+  int n;
+  __device__ __forceinline__ Groups(int* base, int count)
+      : row0(base), rows(base + MAX_GROUPS), prefix(base + 2 * MAX_GROUPS),
+        id(reinterpret_cast<uint16_t*>(prefix + MAX_GROUPS + 1)), n(count) {}
+  __device__ __forceinline__ void build(int* scratch, const int* offsets, int n_rows) {
+    const int lane = lane_id();
+    auto rows_of = [&](int g) {
+      const int r0 = __ldg(offsets + g), r1 = __ldg(offsets + g + 1);
+      return group_ok(r0, r1, n_rows) ? r1 - r0 : 0;
+    };
+    warp_sort<32>(scratch, n, [&](int g) { return 8 - tile_height(rows_of(g)) / 32; },
+                  [&](int at, int g) {
+                    row0[at] = __ldg(offsets + g);
+                    rows[at] = rows_of(g);
+                    id[at] = (uint16_t)g;
+                    if (blockIdx.x == 0 && !group_ok(row0[at], __ldg(offsets + g + 1), n_rows))
+                      set_status(MOE_ERR_DEVICE_CHECK);
+                  });
+    __syncwarp();
+    int carry = 0;
+    for (int base = 0; base < n; base += 32) {
+      const int i = base + lane;
+      const int v = i < n ? row_tiles(rows[i]) : 0;
       int incl = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
-      if (g < n) prefix[g] = carry + incl - v;
+      if (i < n) prefix[i] = carry + incl - v;
       carry += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) prefix[n] = carry;
@@ -140,9 +212,10 @@ struct Groups {
 template <bool W_MN>
 __global__ void __launch_bounds__(MM_THREADS, 1)
     k_grouped_mm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                 const __grid_constant__ CUtensorMap tmXs, const Args a) {
+                 const __grid_constant__ CUtensorMap tmX64,
+                 const __grid_constant__ CUtensorMap tmX32, const Args a) {
   using namespace gemmt;   // cluster helpers of the pair kernels
-  constexpr int TF = 256, TR = 256;   // features and rows of a pair's tile
+  constexpr int TF = 256;             // features of a pair's tile
   constexpr int S = STAGES;
   grid_dep_sync();
   extern __shared__ uint8_t smem_raw[];
@@ -161,7 +234,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   const int warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
-  if (warp == 0) gr.build(a.offsets, a.n_rows, TR);
+  if (warp == 0) gr.build(reinterpret_cast<int*>(xpose), a.offsets, a.n_rows);
   if (threadIdx.x == 32) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
@@ -177,7 +250,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     fence_proxy_async_smem();
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
-    tma_prefetch_desc(&tmXs);
+    tma_prefetch_desc(&tmX64);
+    tma_prefetch_desc(&tmX32);
   }
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -192,9 +266,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int n_ft = (a.feats + TF - 1) / TF;
-  const int total = gr.prefix[a.n] * n_ft;
   const int num_kb = (a.contract + 63) / 64;
-  const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
+  const int total = gr.prefix[a.n] * n_ft;
 
   // feature tiles run fastest, so the pairs of one wave share a group's rows in L2
   struct Tile {
@@ -204,10 +277,11 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     Tile t;
     const int rt = tile / n_ft;
     t.ft = tile - rt * n_ft;
-    t.g = gemm::find_group(gr.prefix, a.n, rt);
-    const int at = (rt - gr.prefix[t.g]) * TR;
-    t.row = gr.row0[t.g] + at;
-    t.rows = min(TR, gr.rows[t.g] - at);
+    const int p = gemm::find_group(gr.prefix, a.n, rt);
+    const int height = tile_height(gr.rows[p]), at = (rt - gr.prefix[p]) * height;
+    t.g = gr.id[p];
+    t.row = gr.row0[p] + at;
+    t.rows = min(height, gr.rows[p] - at);
     t.cols = (t.rows + 31) & ~31;
     return t;
   };
@@ -217,13 +291,13 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     if (elect_one()) {
       int it = 0;
       bool ok = true;
-      for (int tile = tile0; tile < total && ok; tile += tstep) {
+      for (int w = 0, tile; (tile = tile_of(w)) < total && ok; ++w) {
         const Tile t = locate(tile);
-        // a tile of few rows takes them with the small box
-        const bool small = t.cols / 2 <= SMALL_ROWS;
-        const CUtensorMap* tx = small ? &tmXs : &tmX;
-        const uint32_t bytes = HALF_STAGE + (small ? SMALL_ROWS * 128u : HALF_STAGE);
-        const int xrow = t.row + (int)rank * (t.cols / 2);
+        // the CTA's rows in boxes of 128, 64 and 32, no more than they need: a
+        // tile of few rows is bound by its loads
+        const int half = t.cols / 2, load = (half + 31) & ~31;
+        const uint32_t bytes = HALF_STAGE + (uint32_t)load * 128u;
+        const int xrow = t.row + (int)rank * half;
         const int f = t.ft * TF + (int)rank * 128;
         for (int kb = 0; kb < num_kb; ++kb, ++it) {
           const int s = it % S;
@@ -239,7 +313,14 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
           } else {
             tma_load_3d_pair(&tmW, fl, sw, k, f, t.g);
           }
-          tma_load_2d_pair(tx, fl, sw + HALF_STAGE, k, xrow);
+          uint8_t* sx = sw + HALF_STAGE;
+          if (load == 128) {
+            tma_load_2d_pair(&tmX, fl, sx, k, xrow);
+          } else {
+            if (load & 64) tma_load_2d_pair(&tmX64, fl, sx, k, xrow);
+            if (load & 32)
+              tma_load_2d_pair(&tmX32, fl, sx + (load & 64) * 128, k, xrow + (load & 64));
+          }
         }
       }
       // the copies this CTA issued land before the block may leave (bounded)
@@ -253,7 +334,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     if (leader && elect_one()) {
       int it = 0, tcount = 0;
       bool ok = true;
-      for (int tile = tile0; tile < total && ok; tile += tstep, ++tcount) {
+      for (int tile; (tile = tile_of(tcount)) < total && ok; ++tcount) {
         const Tile t = locate(tile);
         const uint32_t idesc = umma_idesc(1, TF, t.cols) | (W_MN ? (1u << 15) : 0u);
         const int acc = tcount & 1;
@@ -299,7 +380,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     const uint32_t tempty_leader0 = mapa(smem_u32(&tempty[0]), 0);
     const uint32_t tempty_leader1 = mapa(smem_u32(&tempty[1]), 0);
     int tcount = 0;
-    for (int tile = tile0; tile < total; tile += tstep, ++tcount) {
+    for (int tile; (tile = tile_of(tcount)) < total; ++tcount) {
       const Tile t = locate(tile);
       const int acc = tcount & 1;
       const uint32_t use = (uint32_t)(tcount >> 1);
@@ -341,14 +422,15 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
 }
 
 // dW tile of 256 output features (d_out, the UMMA M side) x 256 input features
-// (d_in); both operands MN-major.  tmC: [G, d_out, d_in], 32 x 32 boxes.
+// (d_in); both operands MN-major.  tmC: [G, d_out, d_in], boxes of 32 rows x
+// 128 bytes.
 template <bool OUT_BF16>
 __global__ void __launch_bounds__(DW_THREADS, 1)
     k_grouped_dw(const __grid_constant__ CUtensorMap tmDy, const __grid_constant__ CUtensorMap tmX,
                  const __grid_constant__ CUtensorMap tmC, const Args a) {
   using namespace gemmt;
   constexpr int TO = 256, TI = 256;
-  constexpr int S = STAGES;
+  constexpr int S = DW_STAGES;
   constexpr uint32_t BOX = gbwd::MN_BOX_BYTES;    // 64 rows x 64 features
   static_assert(4 * BOX == STAGE_BYTES, "two boxes of either operand per CTA");
   grid_dep_sync();
@@ -362,21 +444,35 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint64_t* tail = drain + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + S);
+  uint64_t* peer_tail = tail + S;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(peer_tail + S);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint16_t* sorted = reinterpret_cast<uint16_t*>(tmem_slot + 4);
 
   const int warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
+  auto rows_of = [&](int g) {
+    const int r0 = __ldg(a.offsets + g), r1 = __ldg(a.offsets + g + 1);
+    return group_ok(r0, r1, a.n_rows) ? r1 - r0 : 0;
+  };
+  // groups of many rows first, by the upper bits of their count: four classes
+  // for each power of two
+  const bool in_order = a.n > DW_SORTED;
+  if (warp == 0 && !in_order)
+    warp_sort<160>(reinterpret_cast<int*>(store_buf), a.n, [&](int g) {
+      return 148 - (int)((__float_as_uint((float)rows_of(g) + 1.0f) >> 21) - (127u << 2));
+    }, [&](int at, int g) { sorted[at] = (uint16_t)g; });
   if (threadIdx.x == 32) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 2);      // both CTAs' producers, or both CTAs' tail warps
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&tail[s], 1);
+      mbar_init(&peer_tail[s], 1);
     }
     for (int j = 0; j < 2; ++j) {
       mbar_init(&tfull[j], 1);
-      mbar_init(&tempty[j], 2 * 4 * 32);
+      mbar_init(&tempty[j], 2 * DW_EPI_WARPS * 32);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -401,20 +497,19 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
   const int n_it = (a.d_in + TI - 1) / TI, n_ot = (a.d_out + TO - 1) / TO;
   const int per_group = n_it * n_ot;
   const int total = a.n * per_group;
-  const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
 
   struct Tile {
     int g, ot, it, row, rows, nkb, cols;
   };
   auto locate = [&](int tile) {
     Tile t;
-    t.g = tile / per_group;
-    const int l = tile - t.g * per_group;
+    const int at = tile / per_group;
+    t.g = in_order ? at : sorted[at];
+    const int l = tile - at * per_group;
     t.ot = l / n_it;
     t.it = l - t.ot * n_it;
     t.row = __ldg(a.offsets + t.g);
-    const int end = __ldg(a.offsets + t.g + 1);
-    t.rows = group_ok(t.row, end, a.n_rows) ? end - t.row : 0;
+    t.rows = rows_of(t.g);
     t.nkb = (t.rows + 63) / 64;
     t.cols = (min(TI, a.d_in - t.it * TI) + 31) & ~31;
     return t;
@@ -429,7 +524,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     if (elect_one()) {
       int it = 0;
       bool ok = true;
-      for (int tile = tile0; tile < total && ok; tile += tstep) {
+      for (int w = 0, tile; (tile = tile_of(w)) < total && ok; ++w) {
         const Tile t = locate(tile);
         if (idle(t)) continue;
         const int o = t.ot * TO + (int)rank * 128;
@@ -449,7 +544,6 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
           } else {
             const uint32_t fl = mapa(smem_u32(&full[s]), 0);
             if (leader) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
-            else mbar_arrive_cluster(fl);
             tma_load_2d_pair(&tmDy, fl, sa, o, r);
             tma_load_2d_pair(&tmDy, fl, sa + BOX, o + 64, r);
             tma_load_2d_pair(&tmX, fl, sa + 2 * BOX, i, r);
@@ -469,14 +563,15 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
         if (!group_ok(a.offsets[g], a.offsets[g + 1], a.n_rows)) set_status(MOE_ERR_DEVICE_CHECK);
     int it = 0;
     uint32_t uses = 0;       // parity of the uses of each stage's tail barrier
-    for (int tile = tile0; tile < total; tile += tstep) {
+    for (int w = 0, tile; (tile = tile_of(w)) < total; ++w) {
       const Tile t = locate(tile);
       if (idle(t)) continue;
       it += t.nkb;
       if (t.nkb == 0 || !is_tail(t, t.nkb - 1)) continue;
       const int s = (it - 1) % S;
-      if (!mbar_wait(&tail[s], (uses >> s) & 1u, abort_flag)) break;
+      const uint32_t ph = (uses >> s) & 1u;
       uses ^= 1u << s;
+      if (!mbar_wait(&tail[s], ph, abort_flag)) break;
       const int first = t.rows - (t.nkb - 1) * 64, end = (first + 15) & ~15;
       uint8_t* sa = smem + (size_t)s * STAGE_BYTES;
       // a row is one 128-byte line of each of the four boxes; the swizzle
@@ -487,17 +582,21 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        if (leader) mbar_arrive(&full[s]);
-        else mbar_arrive_cluster(mapa(smem_u32(&full[s]), 0));
+      if (!leader) {
+        if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&peer_tail[s]), 0));
+        continue;
       }
+      if (!mbar_wait(&peer_tail[s], ph, abort_flag)) break;
+      asm volatile("fence.acq_rel.cluster;" ::: "memory");   // the peer's cleared lines
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer (leader)
     if (leader && elect_one()) {
       int it = 0, tcount = 0;
       bool ok = true;
-      for (int tile = tile0; tile < total && ok; tile += tstep) {
+      for (int w = 0, tile; (tile = tile_of(w)) < total && ok; ++w) {
         const Tile t = locate(tile);
         if (idle(t)) continue;
         const uint32_t idesc = umma_idesc(1, TO, t.cols) | (1u << 15) | (1u << 16);
@@ -511,8 +610,6 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
           const int s = it % S;
           const uint32_t ph = (uint32_t)(it / S) & 1u;
           if (!mbar_wait(&full[s], ph, abort_flag)) { ok = false; break; }
-          // the peer's cleared lines, released by its tail warp's arrival
-          if (is_tail(t, kb)) asm volatile("fence.acq_rel.cluster;" ::: "memory");
           tc_fence_after();
           const uint32_t sa = smem_u32(smem + (size_t)s * STAGE_BYTES);
           const uint64_t ad = gbwd::umma_desc_sw128_mn(sa);
@@ -540,14 +637,16 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ epilogue (both CTAs)
-    // 32 x 32 blocks through shared memory to TMA stores (or, accumulating,
-    // TMA additions: each element of dW is added to once), which clip the edges.
-    const int q = warp - 4;
-    uint8_t* stg = store_buf + (size_t)q * 2 * 4096;
+    // Blocks of 32 rows x 128 bytes through shared memory to TMA stores (or,
+    // accumulating, TMA additions: each element of dW is added to once), which
+    // clip the edges.
+    // Warp w reads TMEM lanes 32 (w % 4) .. +31 and every other block.
+    const int ew = warp - 4, q = warp & 3, par = ew >> 2;
+    uint8_t* stg = store_buf + (size_t)ew * DW_STAGING;
     const uint32_t tempty_leader0 = mapa(smem_u32(&tempty[0]), 0);
     const uint32_t tempty_leader1 = mapa(smem_u32(&tempty[1]), 0);
     int tcount = 0, nst = 0;
-    for (int tile = tile0; tile < total; tile += tstep) {
+    for (int w = 0, tile; (tile = tile_of(w)) < total; ++w) {
       const Tile t = locate(tile);
       if (idle(t)) continue;
       const int acc = tcount & 1;
@@ -558,43 +657,43 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
       const bool any = t.rows > 0;
       const int o = t.ot * TO + (int)rank * 128 + q * 32;   // the warp's first output feature
-      const int chunks = o < a.d_out ? t.cols / 32 : 0;
-      for (int c = 0; c < chunks; ++c, ++nst) {
-        uint32_t va[16], vb[16];
-        tmem_ld16_nowait(tb + (uint32_t)(32 * c), va);
-        tmem_ld16_nowait(tb + (uint32_t)(32 * c + 16), vb);
-        tmem_wait_ld2(va, vb);
-        uint8_t* buf = stg + (size_t)(nst & 1) * 4096;
-        // the store issued from this buffer two chunks ago has read it
+      constexpr int W = OUT_BF16 ? 64 : 32;                 // columns of a block
+      const int chunks = o < a.d_out ? (t.cols + W - 1) / W : 0;
+      for (int c = par; c < chunks; c += 2, ++nst) {
+        uint8_t* buf = stg + (size_t)(nst & 1) * (DW_STAGING / 2);
+        // the store issued from this buffer before the last has read it
         if (lane == 0) bulk_wait_group_read<1>();
         __syncwarp();
-        if (OUT_BF16) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t* src = j < 2 ? &va[8 * j] : &vb[8 * (j - 2)];
+        for (int h = 0; h < W / 32; ++h) {
+          uint32_t v[2][16];
+          tmem_ld16_nowait(tb + (uint32_t)(W * c + 32 * h), v[0]);
+          tmem_ld16_nowait(tb + (uint32_t)(W * c + 32 * h + 16), v[1]);
+          tmem_wait_ld2(v[0], v[1]);
+          // row `lane`, 16-byte piece j at j ^ (row % 8) (128-byte swizzle)
+#pragma unroll
+          for (int j = 0; j < (OUT_BF16 ? 4 : 8); ++j) {
             uint32_t w4[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w4[i] = any ? gemm::pack_bf16x2(__uint_as_float(src[2 * i]),
-                                              __uint_as_float(src[2 * i + 1]))
-                          : 0u;
-            *reinterpret_cast<uint4*>(buf + lane * 64 + j * 16) =
+            for (int i = 0; i < 4; ++i) {
+              if (OUT_BF16) {
+                const int k = 8 * j + 2 * i;
+                w4[i] = gemm::pack_bf16x2(__uint_as_float(v[k >> 4][k & 15]),
+                                          __uint_as_float(v[k >> 4][(k & 15) + 1]));
+              } else {
+                w4[i] = v[j >> 2][4 * (j & 3) + i];
+              }
+              if (!any) w4[i] = 0u;
+            }
+            *reinterpret_cast<uint4*>(buf + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4)) =
                 make_uint4(w4[0], w4[1], w4[2], w4[3]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t* src = j < 4 ? &va[4 * j] : &vb[4 * (j - 4)];
-            const uint4 v = any ? make_uint4(src[0], src[1], src[2], src[3])
-                                : make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = v;
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (a.accumulate) tma_add_3d(&tmC, buf, t.it * TI + 32 * c, o, t.g);
-          else gbwd::tma_store_3d(&tmC, buf, t.it * TI + 32 * c, o, t.g);
+          if (a.accumulate) tma_add_3d(&tmC, buf, t.it * TI + W * c, o, t.g);
+          else gbwd::tma_store_3d(&tmC, buf, t.it * TI + W * c, o, t.g);
           bulk_commit_group();
         }
       }

@@ -6,10 +6,10 @@
 
 namespace {
 
-// Tensor map of rank 2 or 3 over a contiguous array, 128-byte swizzle unless
-// `plain`; dims innermost first.
+// Tensor map of rank 2 or 3 over a contiguous array, 128-byte swizzle; dims
+// innermost first.
 moe_status grouped_map(CUtensorMap* m, const void* base, bool f32, int rank, const uint64_t* dims,
-                       const uint32_t* box, bool plain = false) {
+                       const uint32_t* box) {
   const uint64_t esz = f32 ? 4 : 2;
   cuuint64_t n[3], strides[2];
   cuuint32_t b[3], one[3] = {1, 1, 1};
@@ -23,7 +23,7 @@ moe_status grouped_map(CUtensorMap* m, const void* base, bool f32, int rank, con
   const CUresult r = g_encode(
       m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
       (cuuint32_t)rank, const_cast<void*>(base), n, strides, b, one,
-      CU_TENSOR_MAP_INTERLEAVE_NONE, plain ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     snprintf(t_errmsg, sizeof(t_errmsg), "cuTensorMapEncodeTiled (grouped): CUresult %d (inner "
@@ -48,11 +48,11 @@ moe_status launch_grouped_mm(bool dx, int32_t G, int32_t R, int32_t d_in, int32_
   const uint64_t wdims[3] = {(uint64_t)d_in, (uint64_t)d_out, (uint64_t)G};
   const uint32_t wbox[3] = {64, dx ? 64u : 128u, 1};
   const uint64_t xdims[2] = {contract, (uint64_t)R};
-  const uint32_t xbox[2] = {64, 128}, sbox[2] = {64, grouped::SMALL_ROWS};
-  CUtensorMap tw, tx, ts;
+  const uint32_t xbox[3][2] = {{64, 128}, {64, 64}, {64, 32}};
+  CUtensorMap tw, tx[3];
   moe_status rc = grouped_map(&tw, w, false, 3, wdims, wbox);
-  if (rc == MOE_OK) rc = grouped_map(&tx, rows, false, 2, xdims, xbox);
-  if (rc == MOE_OK) rc = grouped_map(&ts, rows, false, 2, xdims, sbox);
+  for (int i = 0; i < 3 && rc == MOE_OK; ++i)
+    rc = grouped_map(&tx[i], rows, false, 2, xdims, xbox[i]);
   if (rc != MOE_OK) return rc;
   grouped::Args a;
   memset(&a, 0, sizeof(a));
@@ -70,7 +70,7 @@ moe_status launch_grouped_mm(bool dx, int32_t G, int32_t R, int32_t d_in, int32_
   cudaLaunchAttribute attr[2];
   rc = pair_config(dx ? 5 : 4, k, grouped::MM_THREADS, grouped::MM_SMEM, tiles, st, &cfg, attr);
   if (rc != MOE_OK) return rc;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, tw, tx, ts, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, tw, tx[0], tx[1], tx[2], a);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "k_grouped_mm");
 }
 
@@ -123,11 +123,11 @@ moe_status moe_grouped_mm_dw(int32_t n_groups, int32_t n_rows, int32_t d_in, int
   const uint64_t ydims[2] = {(uint64_t)d_out, (uint64_t)n_rows};
   const uint64_t xdims[2] = {(uint64_t)d_in, (uint64_t)n_rows};
   const uint64_t cdims[3] = {(uint64_t)d_in, (uint64_t)d_out, (uint64_t)n_groups};
-  const uint32_t box[2] = {64, 64}, cbox[3] = {32, 32, 1};
+  const uint32_t box[2] = {64, 64}, cbox[3] = {bf16_grads ? 64u : 32u, 32, 1};
   CUtensorMap ty, tx, tc;
   rc = grouped_map(&ty, dy, false, 2, ydims, box);
   if (rc == MOE_OK) rc = grouped_map(&tx, x, false, 2, xdims, box);
-  if (rc == MOE_OK) rc = grouped_map(&tc, dw, !bf16_grads, 3, cdims, cbox, bf16_grads != 0);
+  if (rc == MOE_OK) rc = grouped_map(&tc, dw, !bf16_grads, 3, cdims, cbox);
   if (rc != MOE_OK) return rc;
   grouped::Args a;
   memset(&a, 0, sizeof(a));
