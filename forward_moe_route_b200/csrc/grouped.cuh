@@ -48,13 +48,13 @@ namespace moe {
 namespace grouped {
 
 constexpr int MAX_GROUPS = 1024;
-constexpr int STAGES = 6;                      // k_grouped_mm; DW_STAGES in k_grouped_dw
+constexpr int STAGES = 6;
 constexpr uint32_t STAGE_BYTES = 32768;        // 16 KB of either operand per CTA
 constexpr uint32_t HALF_STAGE = STAGE_BYTES / 2;
 constexpr int ACC_COLS = 256;
 constexpr int TMEM_COLS = 512;
 constexpr uint32_t BAR_BYTES = (4 * STAGES + 6) * 8 + 16;
-constexpr uint32_t TAB_BYTES = (3 * MAX_GROUPS + 1) * 4 + MAX_GROUPS * 2 + 12;
+constexpr uint32_t TAB_BYTES = (3 * MAX_GROUPS + 1) * 4 + 12;
 
 // ---- rows on the N side -------------------------------------------------------------
 constexpr int MM_THREADS = 384;
@@ -66,13 +66,11 @@ constexpr uint32_t MM_SMEM = 1024 + STAGES * STAGE_BYTES + MM_EPI_WARPS * MM_XPO
 // ---- weight gradients -----------------------------------------------------------------
 constexpr int DW_THREADS = 384;
 constexpr int DW_EPI_WARPS = 8;
-constexpr int DW_STAGES = 5;
-// a warp's staging: two blocks of 32 rows of 128 bytes
-constexpr uint32_t DW_STAGING = 8192;
+// a warp's staging: one block of 32 rows of 128 bytes.  (Two of them and five
+// stages instead of six: the same on groups of 384 rows, 5% slower on 1024.)
+constexpr uint32_t DW_STAGING = 4096;
 constexpr uint32_t DW_STORE = DW_EPI_WARPS * DW_STAGING;
-constexpr int DW_SORTED = 512;                 // most groups taken in order of their rows
-constexpr uint32_t DW_SMEM = 1024 + DW_STAGES * STAGE_BYTES + DW_STORE + BAR_BYTES +
-                             DW_SORTED * 2;
+constexpr uint32_t DW_SMEM = 1024 + STAGES * STAGE_BYTES + DW_STORE + BAR_BYTES;
 static_assert(MM_SMEM <= 232448 && DW_SMEM <= 232448, "shared memory of one block");
 
 struct Args {
@@ -106,60 +104,10 @@ __device__ __forceinline__ bool group_ok(int r0, int r1, int n_rows) {
   return r0 >= 0 && r1 >= r0 && r1 <= n_rows;
 }
 
-// Stable counting sort of n groups by key(g) in [0, KEYS), by one warp with
-// `slot` [KEYS] in shared memory: put(place, g) is called once for each group,
-// lower keys first, equal keys in the groups' order, so that every block comes
-// to the same list.
-template <int KEYS, typename Key, typename Put>
-__device__ __forceinline__ void warp_sort(int* slot, int n, Key key, Put put) {
-  static_assert(KEYS % 32 == 0, "");
-  const int lane = lane_id();
-  for (int k = lane; k < KEYS; k += 32) slot[k] = 0;
-  __syncwarp();
-  // visit(g, k, place) with the place among equal keys, slot[k] moved on
-  auto sweep = [&](auto visit) {
-    for (int base = 0; base < n; base += 32) {
-      const int g = base + lane;
-      const int k = g < n ? key(g) : -1;
-      const uint32_t same = __match_any_sync(0xffffffffu, k);
-      const int rank = __popc(same & ((1u << lane) - 1u));
-      const int from = k >= 0 ? slot[k] : 0;
-      __syncwarp();
-      if (k >= 0) {
-        if (rank == 0) slot[k] = from + __popc(same);
-        visit(g, from + rank);
-      }
-      __syncwarp();
-    }
-  };
-  sweep([](int, int) {});
-  int carry = 0;
-  for (int base = 0; base < KEYS; base += 32) {
-    const int count = slot[base + lane];
-    int incl = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    slot[base + lane] = carry + incl - count;
-    carry += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  __syncwarp();
-  sweep([&](int g, int place) { put(place, g); });
-}
-
-// Tiles of a pair: wave after wave over all pairs, every other wave backwards.
-// The tiles come in order of falling cost, so the pairs' sums differ by less
-// than one tile whatever the groups' loads.
-__device__ __forceinline__ int tile_of(int wave) {
-  const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
-  return wave * pairs + ((wave & 1) ? pairs - 1 - pair : pair);
-}
-
 // k_grouped_mm cuts a group of r rows into ceil(r / 256) row tiles of equal
 // height, rounded up to the 32 rows that the UMMA N goes by (r = 257: 160 + 97,
-// not 256 + 1).
+// not 256 + 1): 5 to 8% faster than full tiles and a rest on uneven groups, as
+// a low tile costs the loads of its weights all the same.
 constexpr int TILE_ROWS = 256;
 __device__ __forceinline__ int row_tiles(int rows) { return (rows + TILE_ROWS - 1) / TILE_ROWS; }
 __device__ __forceinline__ int tile_height(int rows) {
@@ -167,42 +115,34 @@ __device__ __forceinline__ int tile_height(int rows) {
   return n ? ((rows + n - 1) / n + 31) & ~31 : 0;
 }
 
-// The group list in shared memory, in order of falling tile height: first row,
-// rows and number of each group, and the prefix of the row tiles.  One warp
-// builds it.
+// The group list in shared memory: first row and rows of each group, and the
+// prefix of its row tiles.  One warp builds it.
 struct Groups {
   int *row0, *rows, *prefix;   // [n], [n], [n + 1]
-  uint16_t* id;                // [n]
   int n;
   __device__ __forceinline__ Groups(int* base, int count)
-      : row0(base), rows(base + MAX_GROUPS), prefix(base + 2 * MAX_GROUPS),
-        id(reinterpret_cast<uint16_t*>(prefix + MAX_GROUPS + 1)), n(count) {}
-  __device__ __forceinline__ void build(int* scratch, const int* offsets, int n_rows) {
+      : row0(base), rows(base + MAX_GROUPS), prefix(base + 2 * MAX_GROUPS), n(count) {}
+  __device__ __forceinline__ void build(const int* offsets, int n_rows) {
     const int lane = lane_id();
-    auto rows_of = [&](int g) {
-      const int r0 = __ldg(offsets + g), r1 = __ldg(offsets + g + 1);
-      return group_ok(r0, r1, n_rows) ? r1 - r0 : 0;
-    };
-    warp_sort<32>(scratch, n, [&](int g) { return 8 - tile_height(rows_of(g)) / 32; },
-                  [&](int at, int g) {
-                    row0[at] = __ldg(offsets + g);
-                    rows[at] = rows_of(g);
-                    id[at] = (uint16_t)g;
-                    if (blockIdx.x == 0 && !group_ok(row0[at], __ldg(offsets + g + 1), n_rows))
-                      set_status(MOE_ERR_DEVICE_CHECK);
-                  });
-    __syncwarp();
     int carry = 0;
     for (int base = 0; base < n; base += 32) {
-      const int i = base + lane;
-      const int v = i < n ? row_tiles(rows[i]) : 0;
+      const int g = base + lane;
+      int r = 0;
+      if (g < n) {
+        const int r0 = offsets[g], r1 = offsets[g + 1];
+        if (group_ok(r0, r1, n_rows)) r = r1 - r0;
+        else if (blockIdx.x == 0) set_status(MOE_ERR_DEVICE_CHECK);
+        row0[g] = r0;
+        rows[g] = r;
+      }
+      const int v = row_tiles(r);
       int incl = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
-      if (i < n) prefix[i] = carry + incl - v;
+      if (g < n) prefix[g] = carry + incl - v;
       carry += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) prefix[n] = carry;
@@ -234,7 +174,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   const int warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
-  if (warp == 0) gr.build(reinterpret_cast<int*>(xpose), a.offsets, a.n_rows);
+  if (warp == 0) gr.build(a.offsets, a.n_rows);
   if (threadIdx.x == 32) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
@@ -268,6 +208,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   const int n_ft = (a.feats + TF - 1) / TF;
   const int num_kb = (a.contract + 63) / 64;
   const int total = gr.prefix[a.n] * n_ft;
+  const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
 
   // feature tiles run fastest, so the pairs of one wave share a group's rows in L2
   struct Tile {
@@ -279,7 +220,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     t.ft = tile - rt * n_ft;
     const int p = gemm::find_group(gr.prefix, a.n, rt);
     const int height = tile_height(gr.rows[p]), at = (rt - gr.prefix[p]) * height;
-    t.g = gr.id[p];
+    t.g = p;
     t.row = gr.row0[p] + at;
     t.rows = min(height, gr.rows[p] - at);
     t.cols = (t.rows + 31) & ~31;
@@ -291,7 +232,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     if (elect_one()) {
       int it = 0;
       bool ok = true;
-      for (int w = 0, tile; (tile = tile_of(w)) < total && ok; ++w) {
+      for (int tile = tile0; tile < total && ok; tile += tstep) {
         const Tile t = locate(tile);
         // the CTA's rows in boxes of 128, 64 and 32, no more than they need: a
         // tile of few rows is bound by its loads
@@ -334,7 +275,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     if (leader && elect_one()) {
       int it = 0, tcount = 0;
       bool ok = true;
-      for (int tile; (tile = tile_of(tcount)) < total && ok; ++tcount) {
+      for (int tile = tile0; tile < total && ok; tile += tstep, ++tcount) {
         const Tile t = locate(tile);
         const uint32_t idesc = umma_idesc(1, TF, t.cols) | (W_MN ? (1u << 15) : 0u);
         const int acc = tcount & 1;
@@ -380,7 +321,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     const uint32_t tempty_leader0 = mapa(smem_u32(&tempty[0]), 0);
     const uint32_t tempty_leader1 = mapa(smem_u32(&tempty[1]), 0);
     int tcount = 0;
-    for (int tile; (tile = tile_of(tcount)) < total; ++tcount) {
+    for (int tile = tile0; tile < total; tile += tstep, ++tcount) {
       const Tile t = locate(tile);
       const int acc = tcount & 1;
       const uint32_t use = (uint32_t)(tcount >> 1);
@@ -430,7 +371,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                  const __grid_constant__ CUtensorMap tmC, const Args a) {
   using namespace gemmt;
   constexpr int TO = 256, TI = 256;
-  constexpr int S = DW_STAGES;
+  constexpr int S = STAGES;
   constexpr uint32_t BOX = gbwd::MN_BOX_BYTES;    // 64 rows x 64 features
   static_assert(4 * BOX == STAGE_BYTES, "two boxes of either operand per CTA");
   grid_dep_sync();
@@ -447,7 +388,6 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
   uint64_t* peer_tail = tail + S;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(peer_tail + S);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint16_t* sorted = reinterpret_cast<uint16_t*>(tmem_slot + 4);
 
   const int warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_rank();
@@ -456,13 +396,6 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     const int r0 = __ldg(a.offsets + g), r1 = __ldg(a.offsets + g + 1);
     return group_ok(r0, r1, a.n_rows) ? r1 - r0 : 0;
   };
-  // groups of many rows first, by the upper bits of their count: four classes
-  // for each power of two
-  const bool in_order = a.n > DW_SORTED;
-  if (warp == 0 && !in_order)
-    warp_sort<160>(reinterpret_cast<int*>(store_buf), a.n, [&](int g) {
-      return 148 - (int)((__float_as_uint((float)rows_of(g) + 1.0f) >> 21) - (127u << 2));
-    }, [&](int at, int g) { sorted[at] = (uint16_t)g; });
   if (threadIdx.x == 32) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
@@ -497,15 +430,15 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
   const int n_it = (a.d_in + TI - 1) / TI, n_ot = (a.d_out + TO - 1) / TO;
   const int per_group = n_it * n_ot;
   const int total = a.n * per_group;
+  const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
 
   struct Tile {
     int g, ot, it, row, rows, nkb, cols;
   };
   auto locate = [&](int tile) {
     Tile t;
-    const int at = tile / per_group;
-    t.g = in_order ? at : sorted[at];
-    const int l = tile - at * per_group;
+    t.g = tile / per_group;
+    const int l = tile - t.g * per_group;
     t.ot = l / n_it;
     t.it = l - t.ot * n_it;
     t.row = __ldg(a.offsets + t.g);
@@ -524,7 +457,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     if (elect_one()) {
       int it = 0;
       bool ok = true;
-      for (int w = 0, tile; (tile = tile_of(w)) < total && ok; ++w) {
+      for (int tile = tile0; tile < total && ok; tile += tstep) {
         const Tile t = locate(tile);
         if (idle(t)) continue;
         const int o = t.ot * TO + (int)rank * 128;
@@ -563,7 +496,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
         if (!group_ok(a.offsets[g], a.offsets[g + 1], a.n_rows)) set_status(MOE_ERR_DEVICE_CHECK);
     int it = 0;
     uint32_t uses = 0;       // parity of the uses of each stage's tail barrier
-    for (int w = 0, tile; (tile = tile_of(w)) < total; ++w) {
+    for (int tile = tile0; tile < total; tile += tstep) {
       const Tile t = locate(tile);
       if (idle(t)) continue;
       it += t.nkb;
@@ -596,7 +529,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     if (leader && elect_one()) {
       int it = 0, tcount = 0;
       bool ok = true;
-      for (int w = 0, tile; (tile = tile_of(w)) < total && ok; ++w) {
+      for (int tile = tile0; tile < total && ok; tile += tstep) {
         const Tile t = locate(tile);
         if (idle(t)) continue;
         const uint32_t idesc = umma_idesc(1, TO, t.cols) | (1u << 15) | (1u << 16);
@@ -642,11 +575,10 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     // clip the edges.
     // Warp w reads TMEM lanes 32 (w % 4) .. +31 and every other block.
     const int ew = warp - 4, q = warp & 3, par = ew >> 2;
-    uint8_t* stg = store_buf + (size_t)ew * DW_STAGING;
     const uint32_t tempty_leader0 = mapa(smem_u32(&tempty[0]), 0);
     const uint32_t tempty_leader1 = mapa(smem_u32(&tempty[1]), 0);
-    int tcount = 0, nst = 0;
-    for (int w = 0, tile; (tile = tile_of(w)) < total; ++w) {
+    int tcount = 0;
+    for (int tile = tile0; tile < total; tile += tstep) {
       const Tile t = locate(tile);
       if (idle(t)) continue;
       const int acc = tcount & 1;
@@ -659,10 +591,10 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
       const int o = t.ot * TO + (int)rank * 128 + q * 32;   // the warp's first output feature
       constexpr int W = OUT_BF16 ? 64 : 32;                 // columns of a block
       const int chunks = o < a.d_out ? (t.cols + W - 1) / W : 0;
-      for (int c = par; c < chunks; c += 2, ++nst) {
-        uint8_t* buf = stg + (size_t)(nst & 1) * (DW_STAGING / 2);
-        // the store issued from this buffer before the last has read it
-        if (lane == 0) bulk_wait_group_read<1>();
+      for (int c = par; c < chunks; c += 2) {
+        uint8_t* buf = store_buf + (size_t)ew * DW_STAGING;
+        // the last store has read the block
+        if (lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
 #pragma unroll
         for (int h = 0; h < W / 32; ++h) {
