@@ -21,6 +21,7 @@
 // block.  Row sums are warp shuffles, then one shared-memory exchange.
 #pragma once
 
+#include "bulk.cuh"
 #include "common.cuh"
 
 namespace moe {
@@ -68,6 +69,33 @@ __device__ __forceinline__ void store_vec(E* p, const float (&v)[V]) {
     *p = Elem<E>::put(v[0]);
   }
 }
+
+// V elements as they are stored: half the registers of their fp32 values in bf16.
+template <typename E, int V>
+struct Raw {
+  static constexpr int WORDS = V == 1 ? 1 : 4;
+  uint32_t word[WORDS];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) word[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const E* p) {
+    if constexpr (V == 1) {
+      word[0] = 0u;
+      *reinterpret_cast<E*>(word) = *p;
+    } else {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      word[0] = x.x;
+      word[1] = x.y;
+      word[2] = x.z;
+      word[3] = x.w;
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (sizeof(E) == 4) return __uint_as_float(word[j]);
+    else return __uint_as_float((j & 1) ? word[j >> 1] & 0xffff0000u : word[j >> 1] << 16);
+  }
+};
 
 // The threads that share a row: one warp of the block (tpr = 32), or the block.
 // Sums over them; `red` is double-buffered, so one barrier per sum suffices:
@@ -217,140 +245,284 @@ struct BwdArgs {
   int rows;              // tokens of a unit
   int units;
   int tpr;
+  int alone;             // 1: a unit is one row group's, 0: the block's row groups share it
+  int stages;            // rows of the ring of each row group
   float eps, res;
 };
 
-// A unit is a run of tokens of one gate row; units are strided over the
-// blocks.  Every thread keeps the sums of its columns over the unit's tokens
-// (the gate's gradient) and over all of the block's (the weight's); both are
-// joined in a fixed order, so two runs agree bit for bit.  With one warp per
-// row a block's row groups share the unit's tokens and join their sums in
-// shared memory at the unit's end.
+// A unit is a run of tokens of one gate row; units are strided over the blocks,
+// which share each among their row groups (or, when gate rows have few tokens,
+// over the row groups).  Every thread sums upstream * n of its columns over the
+// unit, s.  The unit's share of the gate's gradient is w s and of the weight's
+// gate s, so one sum serves both: a unit that is a whole gate row writes its
+// gate gradient and adds gate s to the thread's sum for dw, the units of a split
+// gate row leave s to the join.  All sums are joined in a fixed order: two runs
+// agree bit for bit.
+//
+// Rows of whole vectors reach the threads through shared memory: each row group
+// keeps `stages` rows of its operands in flight with bulk copies, across units,
+// and refills a stage as soon as its threads have the row in registers (behind
+// the barrier of the row's sums).
+//
+// What a row costs beside its elements (the barrier, the sums, the waits) is
+// about 80 instructions a thread, so a thread takes up to 4 vectors of a row,
+// which it holds as they are stored, and a block of up to 512 threads several
+// rows at a time.  One block on each SM.
+constexpr int BWD_THREADS = 512;
 template <typename E, int V, int VPT, bool GATE>
-__global__ void __launch_bounds__(VPT* V > 8 ? 512 : MAX_THREADS) k_norm_bwd(const BwdArgs a) {
+__global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
+  constexpr bool RING = V > 1;
   grid_dep_sync();
-  extern __shared__ float joined[];   // one warp per row: [row groups][d]
-  __shared__ float2 red[2][32];
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ float red[2][2][32];
+  __shared__ uint64_t full[16][8];
+  __shared__ int abort_word;
   const int rows_here = blockDim.x / a.tpr, mine = threadIdx.x / a.tpr;
-  RowGroup g{a.tpr, (int)threadIdx.x % a.tpr, red, 0};
+  const int tid = (int)threadIdx.x % a.tpr;
   const int d = a.d;
   const E* w = static_cast<const E*>(a.w);
-  float aw[VPT][V];
+  const uint32_t row_bytes = (uint32_t)d * sizeof(E);
+  constexpr bool ADD = !GATE;               // the residual's gradient joins moe_norm's only
+  const bool add = ADD && a.add != nullptr;
+  const int parts = add ? 3 : 2;
+  const uint32_t stage_bytes = parts * row_bytes;
+  uint8_t* ring = dyn + (size_t)mine * a.stages * stage_bytes;
+  // behind the ring: the row groups' sums [rows_here][d], and with whole gate
+  // rows shared by the block the sum for dw [d]
+  float* joined = reinterpret_cast<float*>(
+      dyn + (RING ? (size_t)rows_here * a.stages * stage_bytes : 0));
+  const bool keep = GATE && a.split == 1;   // dw collected over the units
+  float* acc = a.alone ? joined + mine * d : joined + (rows_here > 1 ? rows_here * d : 0);
+  if (RING) {
+    if (tid == 0)
+      for (int s = 0; s < a.stages; ++s) mbar_init(&full[mine][s], 1);
+    if (threadIdx.x == 0) abort_word = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
+
+  // the rows of this row group, unit after unit
+  struct Place {
+    int unit;
+    long long t, t1;
+  };
+  const int unit_step = a.alone ? (int)gridDim.x * rows_here : (int)gridDim.x;
+  const int first = a.alone ? 0 : mine, step = a.alone ? 1 : rows_here;
+  auto enter = [&](Place& p) {
+    const int k = p.unit / a.split;
+    const long long t0 = (long long)k * a.group + (long long)(p.unit - k * a.split) * a.rows;
+    p.t = t0 + first;
+    p.t1 = min(min(t0 + a.rows, (long long)(k + 1) * a.group), (long long)a.T);
+  };
+  Place here;
+  here.unit = a.alone ? (int)blockIdx.x * rows_here + mine : (int)blockIdx.x;
+  here.t = here.t1 = 0;
+  if (here.unit < a.units) enter(here);
+  // thread 0 of the row group fetches rows ahead
+  Place ahead = here;
+  int into = 0;
+  auto fetch = [&]() {
+    while (ahead.unit < a.units && ahead.t >= ahead.t1) {
+      ahead.unit += unit_step;
+      if (ahead.unit < a.units) enter(ahead);
+    }
+    if (ahead.unit >= a.units) return;
+    uint64_t* bar = &full[mine][into];
+    uint8_t* to = ring + (size_t)into * stage_bytes;
+    if (++into == a.stages) into = 0;
+    mbar_arrive_expect_tx(bar, stage_bytes);
+    const long long at = ahead.t * d;
+    bulk_load_1d(to, static_cast<const E*>(a.v) + at, row_bytes, bar);
+    bulk_load_1d(to + row_bytes, static_cast<const E*>(a.up) + at, row_bytes, bar);
+    if (add) bulk_load_1d(to + 2 * row_bytes, static_cast<const E*>(a.add) + at, row_bytes, bar);
+    ahead.t += step;
+  };
+  if (RING && tid == 0)
+    for (int s = 0; s < a.stages; ++s) fetch();
+
+  const int lane = lane_id(), nw = a.tpr >> 5, w0 = mine * nw;
+  int buf = 0, stage = 0;
+  uint32_t phase = 0;
+  // both sums over the row group; the lower half of a warp reduces x, the upper y
+  auto sum2 = [&](float x, float y) {
+    const bool up_half = lane >= 16;
+    float z = (up_half ? y : x) + __shfl_xor_sync(0xffffffffu, up_half ? x : y, 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    if (a.tpr == 32) {
+      __syncwarp();
+      return make_float2(__shfl_sync(0xffffffffu, z, 0), __shfl_sync(0xffffffffu, z, 16));
+    }
+    if ((lane & 15) == 0) red[buf][lane >> 4][warp_id()] = z;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + mine), "r"(a.tpr) : "memory");
+    x = y = 0.f;
+    for (int i = 0; i < nw; ++i) {
+      x += red[buf][0][w0 + i];
+      y += red[buf][1][w0 + i];
+    }
+    buf ^= 1;
+    return make_float2(x, y);
+  };
+  // f(c, i, q) for the thread's columns, four at a time (one without vectors)
+  constexpr int Q = V == 1 ? 1 : 4;
+  auto columns = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (tid + i * a.tpr) * V;
+      if (c < d)
+#pragma unroll
+        for (int q = 0; q < V; q += Q) f(c + q, i, q);
+    }
+  };
+  float s[VPT][V];
+  // the row groups' s, complete in row group 0's threads
+  auto join = [&]() {
+    if (rows_here == 1) return;
+    __syncthreads();
+    columns([&](int c, int i, int q) {
+#pragma unroll
+      for (int j = 0; j < Q; ++j) joined[mine * d + c + j] = s[i][q + j];
+    });
+    __syncthreads();
+    if (mine == 0)
+      columns([&](int c, int i, int q) {
+        for (int g = 1; g < rows_here; ++g)
+#pragma unroll
+          for (int j = 0; j < Q; ++j) s[i][q + j] += joined[g * d + c + j];
+      });
+  };
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int j = 0; j < V; ++j) aw[i][j] = 0.f;
+    for (int j = 0; j < V; ++j) s[i][j] = 0.f;
+  if (keep && (a.alone || mine == 0))
+    columns([&](int c, int, int) {
+#pragma unroll
+      for (int j = 0; j < Q; ++j) acc[c + j] = 0.f;
+    });
 
-  // the row groups' sums of the block, complete in row group 0's threads
-  auto join = [&](float (&s)[VPT][V]) {
-    if (rows_here == 1) return;
-    __syncthreads();
+  for (; here.unit < a.units; here.unit += unit_step) {
+    enter(here);
+    const int k = here.unit / a.split;
+    const E* gate = GATE ? static_cast<const E*>(a.gate) + (long long)k * d : nullptr;
+    // w (as stored), or w * gate
+    Raw<E, V> wr[GATE ? 1 : VPT];
+    float wg[GATE ? VPT : 1][V];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (g.tid + i * a.tpr) * V;
-      if (c < d)
+      const int c = (tid + i * a.tpr) * V;
+      if (GATE)
 #pragma unroll
-        for (int j = 0; j < V; ++j) joined[mine * d + c + j] = s[i][j];
-    }
-    __syncthreads();
-    if (mine == 0)
+        for (int j = 0; j < V; ++j) s[i][j] = 0.f;
+      if (c < d) {
+        if constexpr (GATE) {
+          Raw<E, V> x, g;
+          x.load(w + c);
+          g.load(gate + c);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = (g.tid + i * a.tpr) * V;
-        if (c < d)
-          for (int q = 1; q < rows_here; ++q)
-#pragma unroll
-            for (int j = 0; j < V; ++j) s[i][j] += joined[q * d + c + j];
+          for (int j = 0; j < V; ++j) wg[i][j] = x.get(j) * g.get(j);
+        } else {
+          wr[i].load(w + c);
+        }
       }
-  };
-
-  for (int unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
-    const int k = unit / a.split;
-    const long long t0 = (long long)k * a.group + (long long)(unit - k * a.split) * a.rows;
-    const long long t1 = min(min(t0 + a.rows, (long long)(k + 1) * a.group), (long long)a.T);
-    float ag[VPT][V];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) ag[i][j] = 0.f;
-    for (long long t = t0 + mine; t < t1; t += rows_here) {
-      float v[VPT][V], up[VPT][V];
+    }
+    auto weight = [&](int i, int j) {
+      if constexpr (GATE) return wg[i][j];
+      else return wr[i].get(j);
+    };
+    for (; here.t < here.t1; here.t += step) {
+      const E* at = reinterpret_cast<const E*>(ring + (size_t)stage * stage_bytes);
+      if (RING) {
+        // a wait that ran out is reported, and the row's results are void
+        mbar_wait(&full[mine][stage], phase, &abort_word);
+        if (++stage == a.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      const E* v_row = RING ? at : static_cast<const E*>(a.v) + here.t * d;
+      const E* up_row = RING ? at + d : static_cast<const E*>(a.up) + here.t * d;
+      const E* add_row = RING ? at + 2 * d : static_cast<const E*>(a.add) + here.t * d;
+      Raw<E, V> v[VPT], up[VPT], more[ADD ? VPT : 1];
       float ss = 0.f, sc = 0.f;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int c = (g.tid + i * a.tpr) * V;
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[i][j] = up[i][j] = 0.f;
+        const int c = (tid + i * a.tpr) * V;
         if (c < d) {
-          load_vec<E, V>(static_cast<const E*>(a.v) + t * d + c, v[i]);
-          load_vec<E, V>(static_cast<const E*>(a.up) + t * d + c, up[i]);
-          float x[V], gt[V];
-          load_vec<E, V>(w + c, x);
-          if (GATE) load_vec<E, V>(static_cast<const E*>(a.gate) + (long long)k * d + c, gt);
+          v[i].load(v_row + c);
+          up[i].load(up_row + c);
+          if constexpr (ADD) {
+            if (add) more[i].load(add_row + c);
+            else more[i].zero();
+          }
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            ss = fmaf(v[i][j], v[i][j], ss);
-            sc = fmaf(v[i][j], up[i][j] * x[j] * (GATE ? gt[j] : 1.f), sc);
+            ss = fmaf(v[i].get(j), v[i].get(j), ss);
+            sc = fmaf(v[i].get(j), up[i].get(j) * weight(i, j), sc);
           }
         }
       }
-      const float2 s = g.sum2(ss, sc);
-      const float r = inv_rms(s.x, d, a.eps);
-      const float m = r * r * (s.y / (float)d);
+      const float2 q = sum2(ss, sc);
+      if (RING && tid == 0) fetch();      // the stage is in registers
+      const float r = inv_rms(q.x, d, a.eps);
+      const float m = r * r * (q.y / (float)d);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int c = (g.tid + i * a.tpr) * V;
+        const int c = (tid + i * a.tpr) * V;
         if (c < d) {
-          float x[V], gt[V], o[V];
-          load_vec<E, V>(w + c, x);
-          if (GATE) load_vec<E, V>(static_cast<const E*>(a.gate) + (long long)k * d + c, gt);
+          float o[V];
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            const float un = up[i][j] * (v[i][j] * r);    // upstream * n
-            aw[i][j] = fmaf(un, GATE ? gt[j] : 1.f, aw[i][j]);
-            if (GATE) ag[i][j] += un;
-            o[j] = r * (up[i][j] * x[j] * (GATE ? gt[j] : 1.f) - v[i][j] * m);
+            s[i][j] = fmaf(up[i].get(j), v[i].get(j) * r, s[i][j]);
+            o[j] = r * (up[i].get(j) * weight(i, j) - v[i].get(j) * m);
+            if constexpr (ADD) o[j] = fmaf(a.res, more[i].get(j), o[j]);
           }
-          if (a.add) {
-            float y[V];
-            load_vec<E, V>(static_cast<const E*>(a.add) + t * d + c, y);
-#pragma unroll
-            for (int j = 0; j < V; ++j) o[j] = fmaf(a.res, y[j], o[j]);
-          }
-          store_vec<E, V>(static_cast<E*>(a.dv) + t * d + c, o);
+          store_vec<E, V>(static_cast<E*>(a.dv) + here.t * d + c, o);
         }
       }
     }
-    if (GATE) {
-      join(ag);
-      if (mine == 0)
+    if (!GATE) continue;
+    if (!a.alone) join();
+    if (!a.alone && mine != 0) continue;
+    if (!keep) {
+      columns([&](int c, int i, int q) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-          const int c = (g.tid + i * a.tpr) * V;
-          if (c < d) {
-            if (a.split == 1) {
-              float x[V];
-              load_vec<E, V>(w + c, x);
-#pragma unroll
-              for (int j = 0; j < V; ++j) x[j] *= ag[i][j];
-              store_vec<E, V>(static_cast<E*>(a.dgate) + (long long)k * d + c, x);
-            } else {
-#pragma unroll
-              for (int j = 0; j < V; ++j) a.part_g[(long long)unit * d + c + j] = ag[i][j];
-            }
-          }
-        }
+        for (int j = 0; j < Q; ++j)
+          a.part_g[(long long)here.unit * d + c + j] = s[i][q + j];
+      });
+      continue;
     }
-  }
-  join(aw);
-  if (mine == 0)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (g.tid + i * a.tpr) * V;
-      if (c < d)
+      const int c = (tid + i * a.tpr) * V;
+      if (c < d) {
+        Raw<E, V> x, g;
+        x.load(w + c);
+        g.load(gate + c);
+        float o[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) a.part_w[(long long)blockIdx.x * d + c + j] = aw[i][j];
+        for (int j = 0; j < V; ++j) {
+          acc[c + j] = fmaf(g.get(j), s[i][j], acc[c + j]);
+          o[j] = x.get(j) * s[i][j];
+        }
+        store_vec<E, V>(static_cast<E*>(a.dgate) + (long long)k * d + c, o);
+      }
     }
+  }
+  if (GATE && !keep) return;
+  if (!GATE) join();
+  else if (a.alone) __syncthreads();
+  if (mine != 0) return;
+  columns([&](int c, int i, int q) {
+#pragma unroll
+    for (int j = 0; j < Q; ++j) {
+      float x = GATE ? acc[c + j] : s[i][q + j];
+      if (GATE && a.alone)
+        for (int g = 1; g < rows_here; ++g) x += joined[g * d + c + j];
+      a.part_w[(long long)blockIdx.x * d + c + j] = x;
+    }
+  });
 }
 
 // Rows too long for the registers of a block (see norm_shape): the same sums
@@ -502,13 +674,14 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_bwd_wide(const BwdArgs a) 
   }
 }
 
-// Column sums of the partial rows: dw from n_part rows (blockIdx.y = 0), and
-// for a split gate the rows of gate row k = blockIdx.y - 1, times w.  A block
-// sums 32 columns with 32 slices of the rows, joined in order.
+// Column sums of the partial rows.  blockIdx.y = 0: dw, from n_part rows; when
+// those are the units of split gate rows, each times its gate (`gate` given).
+// blockIdx.y = k + 1: the gradient of split gate row k, from its units, times w.
+// A block sums 32 columns with 32 slices of the rows, joined in order.
 template <typename E>
 __global__ void __launch_bounds__(1024) k_norm_join(const float* part_w, int n_part, float* dw,
                                                     const float* part_g, int split, const E* w,
-                                                    E* dgate, int d) {
+                                                    const E* gate, E* dgate, int d) {
   grid_dep_sync();
   __shared__ float s[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
@@ -516,8 +689,16 @@ __global__ void __launch_bounds__(1024) k_norm_join(const float* part_w, int n_p
   const float* p = k < 0 ? part_w : part_g + (long long)k * split * d;
   const int n = k < 0 ? n_part : split;
   float v = 0.f;
-  if (c < d)
-    for (int i = threadIdx.y; i < n; i += 32) v += p[(long long)i * d + c];
+  if (c < d) {
+    if (k < 0 && gate) {
+#pragma unroll 4
+      for (int i = threadIdx.y; i < n; i += 32)
+        v = fmaf(p[(long long)i * d + c], Elem<E>::get(gate[(long long)(i / split) * d + c]), v);
+    } else {
+#pragma unroll 4
+      for (int i = threadIdx.y; i < n; i += 32) v += p[(long long)i * d + c];
+    }
+  }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   v = warp_sum(s[threadIdx.x][threadIdx.y]);

@@ -30,10 +30,12 @@ moe_status norm_dims(const moe_norm_desc* s, NormDims* D) {
 }
 
 // How a row is held.  Rows of whole 16-byte vectors are read in vectors
-// (V = 8 bf16 or 4 fp32), others in single elements; a row of up to 128
-// vectors (64 in the backward) belongs to one warp, a longer one to a block
-// with up to `vpt` vectors a thread; rows beyond that take the looping kernels
-// (vpt = 0).
+// (V = 8 bf16 or 4 fp32), others in single elements; rows that do not fit take
+// the looping kernels (vpt = 0).
+// Forward: a row of up to 128 vectors belongs to one warp, a longer one to a
+// block with up to `vpt` vectors a thread.
+// Backward: up to 4 vectors (16 single elements) a thread and as many rows a
+// block as it holds.
 struct NormShape {
   int v, vpt, tpr, threads;
   int rows_here() const { return threads / tpr; }
@@ -44,19 +46,27 @@ NormShape norm_shape(const NormDims& D, bool backward) {
   const bool whole = D.d % D.vec == 0;
   s.v = whole ? D.vec : 1;
   const int64_t n = D.d / s.v;
-  if (whole && n <= (backward ? 64 : 128)) {
+  if (backward) {
+    s.vpt = !whole ? 16 : n <= 32 ? 1 : n <= 64 ? 2 : 4;
+    s.tpr = (int)((n + s.vpt - 1) / s.vpt + 31) / 32 * 32;
+    if (s.tpr > norm::BWD_THREADS) {
+      s.vpt = 0;
+      s.tpr = s.threads = norm::MAX_THREADS;
+      return s;
+    }
+    s.threads = norm::BWD_THREADS / s.tpr * s.tpr;
+    return s;
+  }
+  if (whole && n <= 128) {
     s.vpt = n <= 32 ? 1 : n <= 64 ? 2 : 4;
     s.tpr = 32;
     s.threads = 256;
     return s;
   }
-  // the backward keeps the sums of its columns in registers too: 16 elements a
-  // thread at most, in blocks of up to 512 threads
-  const int widest = whole ? (backward ? 16 / D.vec : 4) : 8;
-  const int most = backward && whole && D.vec * widest > 8 ? 512 : norm::MAX_THREADS;
+  const int widest = whole ? 4 : 8;
   s.vpt = whole ? 2 : 8;
-  if (n > (int64_t)s.vpt * most) s.vpt = widest;
-  if (n > (int64_t)s.vpt * most) {
+  if (n > (int64_t)s.vpt * norm::MAX_THREADS) s.vpt = widest;
+  if (n > (int64_t)s.vpt * norm::MAX_THREADS) {
     s.vpt = 0;
     s.tpr = s.threads = norm::MAX_THREADS;
     return s;
@@ -66,26 +76,67 @@ NormShape norm_shape(const NormDims& D, bool backward) {
   return s;
 }
 
-// How the backward cuts the tokens: units of `rows` tokens, none across two
-// gate rows, about NORM_BLOCKS of them; a gate row of more tokens is split.
-constexpr int64_t NORM_BLOCKS = 592;   // four blocks for each of 148 SMs
+// How the backward cuts the tokens: units, none across two gate rows, one for
+// each block that runs at a time (one on each of 148 SMs, four of the looping
+// kernel).  A gate row of more tokens
+// is split; gate rows of fewer tokens than keep a block's row groups busy are
+// single row groups' units (`alone`).
+constexpr int64_t NORM_SMS = 148;
 struct NormCut {
   int64_t group, rows, split, units, blocks;
+  bool alone;
 };
-NormCut norm_cut(const NormDims& D, int64_t gate_group, int rows_here) {
+NormCut norm_cut(const NormDims& D, int64_t gate_group, const NormShape& s) {
   NormCut c;
   c.group = gate_group && gate_group < D.T ? gate_group : D.T;
-  const int64_t most = (D.T + NORM_BLOCKS - 1) / NORM_BLOCKS;
-  c.rows = most > rows_here ? most : rows_here;
-  if (c.rows > c.group) c.rows = c.group;
-  if (c.group == 0) {
-    c = NormCut{0, 0, 1, 0, 0};
+  if (c.group == 0) return NormCut{0, 0, 1, 0, 0, false};
+  const int64_t most = NORM_SMS * (s.vpt ? 1 : 4);
+  const int64_t here = s.rows_here();
+  c.alone = gate_group && here > 1 && c.group < 4 * here;
+  if (c.alone) {
+    c.rows = c.group;
+    c.split = 1;
+    c.units = (D.T + c.group - 1) / c.group;
+    const int64_t blocks = (c.units + here - 1) / here;
+    c.blocks = blocks < most ? blocks : most;
     return c;
   }
-  c.split = (c.group + c.rows - 1) / c.rows;
+  // units in one to four full waves of blocks, whichever leaves the last block
+  // the fewest rows (a unit costs about as much as four more)
+  const int64_t gates = (D.T + c.group - 1) / c.group;
+  int64_t best = 0;
+  for (int64_t wave = 1; wave <= 4; ++wave) {
+    int64_t split = wave * most / gates;
+    if (split * here > c.group) split = c.group / here;
+    if (split < 1) split = 1;
+    const int64_t rows = (c.group + split - 1) / split;
+    split = (c.group + rows - 1) / rows;
+    const int64_t cost =
+        (gates * split + most - 1) / most * ((rows + here - 1) / here + 4);
+    if (best && cost >= best) continue;
+    best = cost;
+    c.rows = rows;
+    c.split = split;
+  }
   c.units = (D.T + c.group - 1) / c.group * c.split;
-  c.blocks = c.units < NORM_BLOCKS ? c.units : NORM_BLOCKS;
+  c.blocks = c.units < most ? c.units : most;
   return c;
+}
+
+// Rows in flight for each row group, in the shared memory beside the row groups'
+// sums.
+constexpr int64_t kNormSmem = 208 * 1024;
+constexpr int64_t kNormRing = 8;
+// sums of the row groups, and the weight's when blocks share whole gate rows
+int64_t norm_joined(const NormDims& D, const NormShape& s, const NormCut& c, bool gate) {
+  const int64_t keep = gate && c.split == 1 && !c.alone ? 1 : 0;
+  return ((s.rows_here() > 1 ? s.rows_here() : 0) + keep) * D.d * 4;
+}
+int norm_stages(const NormDims& D, const NormShape& s, int parts, int64_t joined) {
+  if (s.v == 1) return 1;
+  const int64_t room = kNormSmem - joined;
+  const int64_t n = room / (s.rows_here() * parts * D.d * (D.bf16 ? 2 : 4));
+  return (int)(n < kNormRing ? n : kNormRing);
 }
 
 struct NormLayout {
@@ -119,35 +170,51 @@ moe_status launch_norm_fwd(const NormShape& s, norm::FwdArgs a, int sms, cudaStr
 }
 
 template <typename E, bool GATE>
-moe_status launch_norm_bwd(const NormShape& s, const NormCut& c, norm::BwdArgs a, float* dw,
-                           cudaStream_t st) {
+moe_status launch_norm_bwd(const NormDims& D, const NormShape& s, const NormCut& c,
+                           norm::BwdArgs a, float* dw, cudaStream_t st) {
   constexpr int VEC = norm::Elem<E>::VEC;
+  const bool wide = s.vpt == 0;
   if (a.T > 0) {
-    auto* k = s.v == 1 ? (s.vpt ? norm::k_norm_bwd<E, 1, 8, GATE>
-                                : norm::k_norm_bwd_wide<E, 1, GATE>)
+    auto* k = s.v == 1 ? (wide ? norm::k_norm_bwd_wide<E, 1, GATE>
+                               : norm::k_norm_bwd<E, 1, 16, GATE>)
+              : wide       ? norm::k_norm_bwd_wide<E, VEC, GATE>
               : s.vpt == 1 ? norm::k_norm_bwd<E, VEC, 1, GATE>
               : s.vpt == 2 ? norm::k_norm_bwd<E, VEC, 2, GATE>
-              : s.vpt == 4 ? norm::k_norm_bwd<E, VEC, 16 / VEC, GATE>
-                           : norm::k_norm_bwd_wide<E, VEC, GATE>;
+                           : norm::k_norm_bwd<E, VEC, 4, GATE>;
     a.tpr = s.tpr;
-    const size_t smem = s.rows_here() > 1 ? (size_t)s.rows_here() * a.d * 4 : 0;
+    size_t smem = 0;
+    if (!wide) {
+      const int parts = a.add ? 3 : 2;
+      smem = (size_t)norm_joined(D, s, c, GATE);
+      a.stages = norm_stages(D, s, parts, (int64_t)smem);
+      if (s.v > 1) smem += (size_t)s.rows_here() * a.stages * parts * a.d * sizeof(E);
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)kNormSmem);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (k_norm_bwd)");
+    }
     const moe_status rc = launch_chain("k_norm_bwd", k, dim3((unsigned)c.blocks),
                                        dim3(s.threads), smem, st, a);
     if (rc != MOE_OK) return rc;
   }
   const int64_t gates = GATE && c.split > 1 ? c.units / c.split : 0;
+  // split gate rows leave one set of sums for both gradients (the looping kernel
+  // keeps the weight's by themselves)
+  const bool shared = gates && !wide;
   return launch_chain("k_norm_join", norm::k_norm_join<E>,
                       dim3((unsigned)((a.d + 31) / 32), (unsigned)(1 + gates)), dim3(32, 32), 0,
-                      st, static_cast<const float*>(a.part_w), (int)c.blocks, dw,
+                      st, static_cast<const float*>(shared ? a.part_g : a.part_w),
+                      (int)(shared ? c.units : c.blocks), dw,
                       static_cast<const float*>(a.part_g), (int)c.split,
-                      static_cast<const E*>(a.w), static_cast<E*>(a.dgate), a.d);
+                      static_cast<const E*>(a.w),
+                      static_cast<const E*>(shared ? a.gate : nullptr),
+                      static_cast<E*>(a.dgate), a.d);
 }
 
 moe_status norm_backward(const moe_norm_desc& desc, const NormDims& D, bool with_gate,
                          norm::BwdArgs a, float* dw, void* ws, size_t ws_bytes,
                          cudaStream_t st) {
   const NormShape s = norm_shape(D, true);
-  const NormCut c = norm_cut(D, with_gate ? desc.gate_group : 0, s.rows_here());
+  const NormCut c = norm_cut(D, with_gate ? desc.gate_group : 0, s);
   NormDims Dg = D;
   if (!with_gate) Dg.n_gate = 0;
   const NormLayout L = norm_layout(Dg, c, s.vpt == 0);
@@ -163,13 +230,14 @@ moe_status norm_backward(const moe_norm_desc& desc, const NormDims& D, bool with
   a.rows = (int)c.rows;
   a.split = (int)c.split;
   a.units = (int)c.units;
+  a.alone = c.alone ? 1 : 0;
   a.eps = desc.eps;
   a.res = desc.res_scale;
   if (D.bf16)
-    return with_gate ? launch_norm_bwd<__nv_bfloat16, true>(s, c, a, dw, st)
-                     : launch_norm_bwd<__nv_bfloat16, false>(s, c, a, dw, st);
-  return with_gate ? launch_norm_bwd<float, true>(s, c, a, dw, st)
-                   : launch_norm_bwd<float, false>(s, c, a, dw, st);
+    return with_gate ? launch_norm_bwd<__nv_bfloat16, true>(D, s, c, a, dw, st)
+                     : launch_norm_bwd<__nv_bfloat16, false>(D, s, c, a, dw, st);
+  return with_gate ? launch_norm_bwd<float, true>(D, s, c, a, dw, st)
+                   : launch_norm_bwd<float, false>(D, s, c, a, dw, st);
 }
 
 // a required pointer: present and 16-byte aligned
@@ -240,9 +308,9 @@ size_t moe_norm_backward_workspace_size(const moe_norm_desc* desc) {
   NormDims plain = D;
   plain.n_gate = 0;
   const size_t without =
-      norm_layout(plain, norm_cut(D, 0, s.rows_here()), s.vpt == 0).total;
+      norm_layout(plain, norm_cut(D, 0, s), s.vpt == 0).total;
   const size_t with =
-      norm_layout(D, norm_cut(D, desc->gate_group, s.rows_here()), s.vpt == 0).total;
+      norm_layout(D, norm_cut(D, desc->gate_group, s), s.vpt == 0).total;
   return with > without ? with : without;
 }
 
