@@ -693,40 +693,50 @@ def moe_expert_ffn_fp8(desc, n_experts: int, groups, n_rows_in: int, n_rows_out:
 
 # ---- norms around the layer, grouped products and the optimiser step -------------------------
 
-def _operand(where: str, name: str, t, numel: int, dtypes, optional: bool = False) -> None:
-    """Refuse a tensor that is missing, strided, short or of another type.  Address arguments
-    (int) pass unchecked."""
-    if t is None:
-        if not optional:
-            raise MoeError(ERR_INVALID_ARG, f"{where}: {name} is missing")
-        return
-    if isinstance(t, int):
-        return
-    if not t.is_contiguous():
-        raise MoeError(ERR_INVALID_ARG, f"{where}: {name} is not contiguous")
-    kind = str(t.dtype).replace("torch.", "")
-    if kind not in dtypes:
-        raise MoeError(ERR_INVALID_ARG, f"{where}: {name} is {kind}, not {' or '.join(dtypes)}")
-    if t.numel() < numel:
-        raise MoeError(ERR_INVALID_ARG,
-                       f"{where}: {name} holds {t.numel()} elements, the call needs {numel}")
+def _refuse(where: str, why: str):
+    raise MoeError(ERR_INVALID_ARG, f"{where}: {why}")
 
 
-def _on_device(where: str, tensors) -> None:
-    """Refuse (name, tensor) pairs that are not on the current device, whose stream the call
-    uses and whose memory its kernels address."""
-    import torch
-    for name, t in tensors:
-        if t is None or isinstance(t, int):
+_KINDS: dict = {}     # torch dtype -> its name
+
+
+def _operands(where: str, specs) -> list:
+    """The addresses of (name, tensor, least elements, type names, optional) operands.  Refuses a
+    tensor that is missing, strided, short, of another type, or not on the current device, whose
+    stream the call uses and whose memory its kernels address.  Addresses (int) pass unchecked."""
+    out, devices = [], set()
+    for name, t, numel, kinds, optional in specs:
+        if t is None:
+            if not optional:
+                _refuse(where, f"{name} is missing")
+            out.append(None)
             continue
-        if not t.is_cuda:
-            raise MoeError(ERR_INVALID_ARG, f"{where}: {name} is not a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise MoeError(ERR_INVALID_ARG,
-                           f"{where}: {name} is on {t.device}, the current device is "
-                           f"cuda:{torch.cuda.current_device()}")
+        if isinstance(t, int):
+            out.append(t)
+            continue
+        dtype = t.dtype
+        kind = _KINDS.get(dtype)
+        if kind is None:
+            kind = _KINDS[dtype] = str(dtype).replace("torch.", "")
+        if kind not in kinds:
+            _refuse(where, f"{name} is {kind}, not {' or '.join(kinds)}")
+        if not t.is_contiguous():
+            _refuse(where, f"{name} is not contiguous")
+        if numel and t.numel() < numel:
+            _refuse(where, f"{name} holds {t.numel()} elements, the call needs {numel}")
+        devices.add(t.get_device())      # -1 on the CPU
+        out.append(t.data_ptr())
+    if devices:
+        import torch
+        current = torch.cuda.current_device() if -1 not in devices else None
+        if len(devices) > 1 or current not in devices:
+            for name, t, *_ in specs:
+                if t is not None and not isinstance(t, int) and t.get_device() != current:
+                    _refuse(where, f"{name} is on {t.device}, not on the current CUDA device")
+    return out
 
 
+_F32, _BF16, _I32, _U8 = ("float32",), ("bfloat16",), ("int32",), ("uint8",)
 _ACT = {DT_F32: ("float32",), DT_BF16: ("bfloat16",)}
 
 
@@ -749,115 +759,96 @@ def norm_backward_workspace(desc: MoeNormDesc, device="cuda"):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _norm_operands(where: str, desc: MoeNormDesc, rows, vectors, dw=None, gates=(), slots=None,
-                   ws=None) -> None:
-    """rows: [T, d] tensors, vectors: [d], gates: [n_gate, d]; all (name, tensor, optional)."""
+def _norm_act(where: str, desc: MoeNormDesc) -> tuple:
+    """(type names of the activations, elements of [T, d], of [d], of the gate)."""
     act = _ACT.get(desc.act_dtype)
     if act is None:
-        raise MoeError(ERR_INVALID_ARG, f"{where}: act_dtype is not F32 or BF16")
+        _refuse(where, "act_dtype is not F32 or BF16")
     T, d, g = desc.T, desc.d, desc.gate_group
-    n_gate = -(-T // g) if g > 0 else 0
-    for name, t, optional in rows:
-        _operand(where, name, t, T * d, act, optional)
-    for name, t, optional in vectors:
-        _operand(where, name, t, d, act, optional)
-    for name, t, optional in gates:
-        _operand(where, name, t, n_gate * d, act, optional)
-    if slots is not None:
-        _operand(where, "y_slots", slots, T * desc.n_slots * d, act)
-    if dw is not None:
-        _operand(where, "dw", dw, d, ("float32",))
-    if ws is not None:
-        _operand(where, "ws", ws, 0, ("uint8",))
-    _on_device(where, [r[:2] for r in (*rows, *vectors, *gates)] +
-               [("y_slots", slots), ("dw", dw), ("ws", ws)])
+    return act, T * d, d, (-(-T // g) if g > 0 else 0) * d
 
 
 def moe_norm(desc, x, w, out, stream=None) -> None:
     """out = x * rsqrt(mean(x^2) + eps) * w, row by row."""
-    _norm_operands("moe_norm", desc, [("x", x, False), ("out", out, False)], [("w", w, False)])
-    _check(_lib.moe_norm(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(out), _stream(stream)),
-           "moe_norm")
+    act, rows, d, _ = _norm_act("moe_norm", desc)
+    p = _operands("moe_norm", (("x", x, rows, act, False), ("w", w, d, act, False),
+                               ("out", out, rows, act, False)))
+    _check(_lib.moe_norm(ctypes.byref(desc), *p, _stream(stream)), "moe_norm")
 
 
 def moe_combine_norm(desc, x_residual, y_slots, w, gate, w_next, h, y, x_next,
                      stream=None) -> None:
     """h = res_scale * x_residual + gate * norm(sum of y_slots) * w, optionally with that sum (y)
     and the next block's x_next = norm(h) * w_next."""
-    _norm_operands("moe_combine_norm", desc,
-                   [("x_residual", x_residual, False), ("h", h, False), ("y", y, True),
-                    ("x_next", x_next, True)], [("w", w, False), ("w_next", w_next, True)],
-                   gates=[("gate", gate, True)], slots=y_slots)
-    _check(_lib.moe_combine_norm(ctypes.byref(desc), _ptr(x_residual), _ptr(y_slots), _ptr(w),
-                                 _ptr(gate), _ptr(w_next), _ptr(h), _ptr(y), _ptr(x_next),
-                                 _stream(stream)), "moe_combine_norm")
+    act, rows, d, gates = _norm_act("moe_combine_norm", desc)
+    p = _operands("moe_combine_norm", (
+        ("x_residual", x_residual, rows, act, False),
+        ("y_slots", y_slots, rows * desc.n_slots, act, False), ("w", w, d, act, False),
+        ("gate", gate, gates, act, True), ("w_next", w_next, d, act, True),
+        ("h", h, rows, act, False), ("y", y, rows, act, True),
+        ("x_next", x_next, rows, act, True)))
+    _check(_lib.moe_combine_norm(ctypes.byref(desc), *p, _stream(stream)), "moe_combine_norm")
 
 
 def moe_norm_backward(desc, x, w, dout, dh, dx, dw, ws, stream=None) -> None:
     """dx = res_scale * dh + the gradient of x through moe_norm for dout; dw of the weight."""
-    _norm_operands("moe_norm_backward", desc,
-                   [("x", x, False), ("dout", dout, False), ("dh", dh, True), ("dx", dx, False)],
-                   [("w", w, False)], dw=dw, ws=ws)
-    _check(_lib.moe_norm_backward(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(dout), _ptr(dh),
-                                  _ptr(dx), _ptr(dw), _ptr(ws),
-                                  ws.numel() if ws is not None else 0, _stream(stream)),
-           "moe_norm_backward")
+    act, rows, d, _ = _norm_act("moe_norm_backward", desc)
+    p = _operands("moe_norm_backward", (
+        ("x", x, rows, act, False), ("w", w, d, act, False), ("dout", dout, rows, act, False),
+        ("dh", dh, rows, act, True), ("dx", dx, rows, act, False), ("dw", dw, d, _F32, False),
+        ("ws", ws, 0, _U8, True)))
+    _check(_lib.moe_norm_backward(ctypes.byref(desc), *p, ws.numel() if ws is not None else 0,
+                                  _stream(stream)), "moe_norm_backward")
 
 
 def moe_combine_norm_backward(desc, y, w, gate, dh, dy, dw, dgate, ws, stream=None) -> None:
     """Gradients of y, w and the gate through moe_combine_norm's h for dh."""
-    _norm_operands("moe_combine_norm_backward", desc,
-                   [("y", y, False), ("dh", dh, False), ("dy", dy, False)], [("w", w, False)],
-                   dw=dw, gates=[("gate", gate, True), ("dgate", dgate, True)], ws=ws)
-    _check(_lib.moe_combine_norm_backward(ctypes.byref(desc), _ptr(y), _ptr(w), _ptr(gate),
-                                          _ptr(dh), _ptr(dy), _ptr(dw), _ptr(dgate), _ptr(ws),
+    act, rows, d, gates = _norm_act("moe_combine_norm_backward", desc)
+    p = _operands("moe_combine_norm_backward", (
+        ("y", y, rows, act, False), ("w", w, d, act, False), ("gate", gate, gates, act, True),
+        ("dh", dh, rows, act, False), ("dy", dy, rows, act, False), ("dw", dw, d, _F32, False),
+        ("dgate", dgate, gates, act, True), ("ws", ws, 0, _U8, True)))
+    _check(_lib.moe_combine_norm_backward(ctypes.byref(desc), *p,
                                           ws.numel() if ws is not None else 0, _stream(stream)),
            "moe_combine_norm_backward")
 
 
-def _grouped_operands(where: str, offsets, rows_in, weights, dtypes, **rows) -> tuple:
-    """Check the tensors of a grouped product; (n_groups, n_rows, d_in, d_out).  rows_in and
-    `rows`: name -> (tensor, "in" or "out") of [n_rows, d_in or d_out]; weights: (name, tensor)."""
-    wname, w = weights
+def _grouped(where: str, function, weight, in_rows, out_rows, offsets, order, *more,
+             stream) -> None:
+    """Check the operands of a grouped product, (name, tensor) each and the weights' type names
+    last in `weight`, and call it with the operands in `order`."""
+    wname, w, kinds = weight
     if w.dim() != 3:
-        raise MoeError(ERR_INVALID_ARG, f"{where}: {wname} must be [n_groups, d_out, d_in]")
+        _refuse(where, f"{wname} must be [n_groups, d_out, d_in]")
     G, d_out, d_in = w.shape
-    n_rows = rows_in.shape[0]
-    _operand(where, wname, w, w.numel(), dtypes)
-    _operand(where, "offsets", offsets, G + 1, ("int32",))
-    for name, (t, side) in rows.items():
-        width = d_in if side == "in" else d_out
-        if t.dim() != 2 or tuple(t.shape) != (n_rows, width):
-            raise MoeError(ERR_INVALID_ARG, f"{where}: {name} must be [{n_rows}, {width}]")
-        _operand(where, name, t, n_rows * width, ("bfloat16",))
-    _on_device(where, [(wname, w), ("offsets", offsets)] + [(k, v[0]) for k, v in rows.items()])
-    return G, n_rows, d_in, d_out
+    n = out_rows[1].shape[0] if out_rows[1].dim() else 0
+    for (name, t), width in ((in_rows, d_in), (out_rows, d_out)):
+        if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width:
+            _refuse(where, f"{name} must be [{n}, {width}]")
+    specs = {wname: (wname, w, 0, kinds, False), "offsets": ("offsets", offsets, G + 1, _I32, False),
+             in_rows[0]: (*in_rows, 0, _BF16, False), out_rows[0]: (*out_rows, 0, _BF16, False)}
+    _check(function(G, n, d_in, d_out, *_operands(where, [specs[k] for k in order]), *more,
+                    _stream(stream)), where)
 
 
 def moe_grouped_mm(x, w, offsets, y, stream=None) -> None:
     """y[r] = w[g] @ x[r] for the rows offsets[g] <= r < offsets[g + 1] of every group g."""
-    dims = _grouped_operands("moe_grouped_mm", offsets, x, ("w", w), ("bfloat16",), x=(x, "in"),
-                             y=(y, "out"))
-    _check(_lib.moe_grouped_mm(*dims, _ptr(x), _ptr(w), _ptr(offsets), _ptr(y),
-                               _stream(stream)), "moe_grouped_mm")
+    _grouped("moe_grouped_mm", _lib.moe_grouped_mm, ("w", w, _BF16), ("x", x), ("y", y), offsets,
+             ("x", "w", "offsets", "y"), stream=stream)
 
 
 def moe_grouped_mm_dx(dy, w, offsets, dx, stream=None) -> None:
     """dx[r] = w[g].T @ dy[r]: the gradient of moe_grouped_mm's rows."""
-    dims = _grouped_operands("moe_grouped_mm_dx", offsets, dy, ("w", w), ("bfloat16",),
-                             dy=(dy, "out"), dx=(dx, "in"))
-    _check(_lib.moe_grouped_mm_dx(*dims, _ptr(dy), _ptr(w), _ptr(offsets), _ptr(dx),
-                                  _stream(stream)), "moe_grouped_mm_dx")
+    _grouped("moe_grouped_mm_dx", _lib.moe_grouped_mm_dx, ("w", w, _BF16), ("dx", dx), ("dy", dy),
+             offsets, ("dy", "w", "offsets", "dx"), stream=stream)
 
 
 def moe_grouped_mm_dw(dy, x, offsets, dw, accumulate: bool = False, stream=None) -> None:
     """dw[g] = sum of dy[r] x[r]^T over the group's rows (fp32 or bf16 by dw's type); with
     accumulate (fp32 only) added to dw."""
-    dims = _grouped_operands("moe_grouped_mm_dw", offsets, dy, ("dw", dw),
-                             ("float32", "bfloat16"), dy=(dy, "out"), x=(x, "in"))
-    _check(_lib.moe_grouped_mm_dw(*dims, _ptr(dy), _ptr(x), _ptr(offsets), _ptr(dw),
-                                  int(dw.element_size() == 2), int(accumulate),
-                                  _stream(stream)), "moe_grouped_mm_dw")
+    _grouped("moe_grouped_mm_dw", _lib.moe_grouped_mm_dw, ("dw", dw, ("float32", "bfloat16")),
+             ("x", x), ("dy", dy), offsets, ("dy", "x", "offsets", "dw"),
+             int(dw.element_size() == 2), int(accumulate), stream=stream)
 
 
 # ---- AdamW over a list of tensors ------------------------------------------------------------
@@ -904,21 +895,18 @@ def adamw_table(p, grad, m, v, p_bf16=None, weight_decay=0.0, m_scale=None,
             raise MoeError(ERR_INVALID_ARG, f"{where}: p[{i}] is missing")
         size = t["p"].numel()
         blocks = -(-size // 128)
-        for name, need, kinds in [("p", size, ("float32",)), ("grad", size, ("float32", "bfloat16")),
-                                  ("m", size, _STATES[bits]), ("v", size, _STATES[bits]),
-                                  ("m_scale", blocks, ("float32",)),
-                                  ("v_scale", blocks, ("float32",)),
-                                  ("p_bf16", size, ("bfloat16",))]:
-            _operand(where, f"{name}[{i}]", t[name], need, kinds,
-                     name == "p_bf16" or (bits == 32 and name.endswith("scale")))
+        wanted = [("p", size, _F32), ("grad", size, ("float32", "bfloat16")),
+                  ("m", size, _STATES[bits]), ("v", size, _STATES[bits]),
+                  ("m_scale", blocks, _F32), ("v_scale", blocks, _F32), ("p_bf16", size, _BF16)]
+        tensors = [t[name] for name, _, _ in wanted]
+        at = _operands(where, [(f"{name}[{i}]", t[name], need, kinds, name == "p_bf16" or
+                                (bits == 32 and name.endswith("scale")))
+                               for name, need, kinds in wanted])
+        for name, need, _ in wanted:
             if t[name] is not None and t[name].numel() != need:
-                raise MoeError(ERR_INVALID_ARG, f"{where}: {name}[{i}] holds {t[name].numel()} "
-                                                f"elements, not {need}")
-        tensors = [t[k] for k in ("p", "grad", "m", "v", "m_scale", "v_scale", "p_bf16")]
-        _on_device(where, [(f"tensor {i}", x) for x in tensors])
+                _refuse(where, f"{name}[{i}] holds {t[name].numel()} elements, not {need}")
         held.append(tensors)
-        array[i] = MoeAdamwTensor(*[None if x is None else x.data_ptr() for x in tensors], size,
-                                  t["weight_decay"], int(t["grad"].element_size() == 2))
+        array[i] = MoeAdamwTensor(*at, size, t["weight_decay"], int(t["grad"].element_size() == 2))
     bytes_ = int(_lib.moe_adamw_table_size(array, n))
     if bytes_ == 0:
         raise MoeError(ERR_INVALID_ARG, f"{where}: too many tensors or elements")
@@ -934,12 +922,9 @@ def moe_adamw(desc, table: AdamwTable, step, lr=None, stream=None) -> None:
     element that the kernel reads; lr: None (desc.lr) or a CUDA float32 tensor of one element."""
     if table.state_bits != desc.state_bits:
         raise MoeError(ERR_INVALID_ARG, f"moe_adamw: a table of {table.state_bits}-bit states")
-    step_dev = None if isinstance(step, int) else step
-    if step_dev is not None:
-        _operand("moe_adamw", "step", step_dev, 1, ("int32",))
-    if lr is not None:
-        _operand("moe_adamw", "lr", lr, 1, ("float32",))
-    _on_device("moe_adamw", [("table", table.table), ("step", step_dev), ("lr", lr)])
-    _check(_lib.moe_adamw(ctypes.byref(desc), _ptr(table.table), table.n_tensors, table.n_chunks,
-                          step if step_dev is None else 0, _ptr(step_dev), _ptr(lr),
-                          _stream(stream)), "moe_adamw")
+    on_device = not isinstance(step, int)
+    at = _operands("moe_adamw", (("table", table.table, 0, _U8, False),
+                                 ("step", step if on_device else None, 1, _I32, not on_device),
+                                 ("lr", lr, 1, _F32, True)))
+    _check(_lib.moe_adamw(ctypes.byref(desc), at[0], table.n_tensors, table.n_chunks,
+                          0 if on_device else step, at[1], at[2], _stream(stream)), "moe_adamw")

@@ -151,14 +151,27 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_fwd(const FwdArgs a) {
     float ss = 0.f;
     const E* in = COMBINE ? static_cast<const E*>(a.slots) + t * a.S * d
                           : static_cast<const E*>(a.u) + t * d;
+    const E* gate =
+        COMBINE && a.gate ? static_cast<const E*>(a.gate) + (t / a.gate_group) * d : nullptr;
+    // what follows the first sum is asked for before it, where registers allow
+    constexpr bool EARLY = V > 1 && VPT == 1;
+    Raw<E, V> early[EARLY ? 4 : 1];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (g.tid + i * a.tpr) * V;
 #pragma unroll
       for (int j = 0; j < V; ++j) v[i][j] = 0.f;
       if (c < d) {
+        if constexpr (EARLY) {
+          early[0].load(w + c);
+          if (COMBINE) {
+            early[1].load(static_cast<const E*>(a.u) + t * d + c);
+            if (gate) early[2].load(gate + c);
+            if (a.w_next) early[3].load(static_cast<const E*>(a.w_next) + c);
+          }
+        }
         if (COMBINE) {
-#pragma unroll 4
+#pragma unroll (VPT == 1 ? 8 : 4)
           for (int s = 0; s < a.S; ++s) {
             float x[V];
             load_vec<E, V>(in + (long long)s * d + c, x);
@@ -172,6 +185,15 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_fwd(const FwdArgs a) {
         for (int j = 0; j < V; ++j) ss = fmaf(v[i][j], v[i][j], ss);
       }
     }
+    // V values of operand `which`, whose column c is at p + c
+    auto operand = [&](int which, const E* p, int c, float (&x)[V]) {
+      if constexpr (EARLY) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = early[which].get(j);
+      } else {
+        load_vec<E, V>(p + c, x);
+      }
+    };
     const float r = inv_rms(g.sum(ss), d, a.eps);
     if (!COMBINE) {
 #pragma unroll
@@ -179,7 +201,7 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_fwd(const FwdArgs a) {
         const int c = (g.tid + i * a.tpr) * V;
         if (c < d) {
           float x[V];
-          load_vec<E, V>(w + c, x);
+          operand(0, w, c, x);
 #pragma unroll
           for (int j = 0; j < V; ++j) x[j] = v[i][j] * r * x[j];
           store_vec<E, V>(static_cast<E*>(a.h) + t * d + c, x);
@@ -187,7 +209,6 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_fwd(const FwdArgs a) {
       }
       continue;
     }
-    const E* gate = a.gate ? static_cast<const E*>(a.gate) + (t / a.gate_group) * d : nullptr;
     ss = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -195,12 +216,12 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_fwd(const FwdArgs a) {
       if (c < d) {
         if (a.y) store_vec<E, V>(static_cast<E*>(a.y) + t * d + c, v[i]);
         float x[V], u[V];
-        load_vec<E, V>(w + c, x);
-        load_vec<E, V>(static_cast<const E*>(a.u) + t * d + c, u);
+        operand(0, w, c, x);
+        operand(1, static_cast<const E*>(a.u) + t * d, c, u);
 #pragma unroll
         for (int j = 0; j < V; ++j) v[i][j] = v[i][j] * r * x[j];
         if (gate) {
-          load_vec<E, V>(gate + c, x);
+          operand(2, gate, c, x);
 #pragma unroll
           for (int j = 0; j < V; ++j) v[i][j] *= x[j];
         }
@@ -219,7 +240,7 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_fwd(const FwdArgs a) {
         const int c = (g.tid + i * a.tpr) * V;
         if (c < d) {
           float x[V];
-          load_vec<E, V>(static_cast<const E*>(a.w_next) + c, x);
+          operand(3, static_cast<const E*>(a.w_next), c, x);
 #pragma unroll
           for (int j = 0; j < V; ++j) x[j] = v[i][j] * rn * x[j];
           store_vec<E, V>(static_cast<E*>(a.x_next) + t * d + c, x);
@@ -287,12 +308,13 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
   const int parts = add ? 3 : 2;
   const uint32_t stage_bytes = parts * row_bytes;
   uint8_t* ring = dyn + (size_t)mine * a.stages * stage_bytes;
-  // behind the ring: the row groups' sums [rows_here][d], and with whole gate
-  // rows shared by the block the sum for dw [d]
+  // the row groups' sums [rows_here][d], in the ring's place when it has run dry
+  // and behind it with gates; with whole gate rows shared by the block the sum
+  // for dw [d] follows
   float* joined = reinterpret_cast<float*>(
-      dyn + (RING ? (size_t)rows_here * a.stages * stage_bytes : 0));
+      dyn + (RING && GATE ? (size_t)rows_here * a.stages * stage_bytes : 0));
   const bool keep = GATE && a.split == 1;   // dw collected over the units
-  float* acc = a.alone ? joined + mine * d : joined + (rows_here > 1 ? rows_here * d : 0);
+  float* acc = a.alone ? joined + mine * d : joined + rows_here * d;
   if (RING) {
     if (tid == 0)
       for (int s = 0; s < a.stages; ++s) mbar_init(&full[mine][s], 1);
@@ -364,43 +386,47 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
     buf ^= 1;
     return make_float2(x, y);
   };
-  // f(c, i, q) for the thread's columns, four at a time (one without vectors)
+  // V / Q accesses of Q floats cover a vector
   constexpr int Q = V == 1 ? 1 : 4;
-  auto columns = [&](auto f) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (tid + i * a.tpr) * V;
-      if (c < d)
-#pragma unroll
-        for (int q = 0; q < V; q += Q) f(c + q, i, q);
-    }
-  };
   float s[VPT][V];
-  // the row groups' s, complete in row group 0's threads
-  auto join = [&]() {
-    if (rows_here == 1) return;
+  // put(c, x) with the sums over the row groups of Q columns from c on, by every
+  // thread of the block for its share of the columns; `mine_in`: the row groups'
+  // sums are in `joined` already
+  auto join = [&](bool mine_in, auto put) {
     __syncthreads();
-    columns([&](int c, int i, int q) {
+    if (!mine_in) {
 #pragma unroll
-      for (int j = 0; j < Q; ++j) joined[mine * d + c + j] = s[i][q + j];
-    });
-    __syncthreads();
-    if (mine == 0)
-      columns([&](int c, int i, int q) {
-        for (int g = 1; g < rows_here; ++g)
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (tid + i * a.tpr) * V;
+        if (c < d)
 #pragma unroll
-          for (int j = 0; j < Q; ++j) s[i][q + j] += joined[g * d + c + j];
-      });
+          for (int q = 0; q < V; q += Q)
+            store_vec<float, Q>(joined + mine * d + c + q,
+                                *reinterpret_cast<const float(*)[Q]>(&s[i][q]));
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x * Q; c < d; c += blockDim.x * Q) {
+      float x[Q];
+      load_vec<float, Q>(joined + c, x);
+      for (int g = 1; g < rows_here; ++g) {
+        float y[Q];
+        load_vec<float, Q>(joined + g * d + c, y);
+#pragma unroll
+        for (int j = 0; j < Q; ++j) x[j] += y[j];
+      }
+      put(c, x);
+    }
   };
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int j = 0; j < V; ++j) s[i][j] = 0.f;
-  if (keep && (a.alone || mine == 0))
-    columns([&](int c, int, int) {
-#pragma unroll
-      for (int j = 0; j < Q; ++j) acc[c + j] = 0.f;
-    });
+  if (keep && a.alone)
+    for (int c = tid; c < d; c += a.tpr) acc[c] = 0.f;
+  else if (keep)
+    for (int c = threadIdx.x; c < d; c += blockDim.x) acc[c] = 0.f;
+  if (keep) __syncthreads();
 
   for (; here.unit < a.units; here.unit += unit_step) {
     enter(here);
@@ -483,46 +509,45 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
       }
     }
     if (!GATE) continue;
-    if (!a.alone) join();
-    if (!a.alone && mine != 0) continue;
-    if (!keep) {
-      columns([&](int c, int i, int q) {
+    // acc += gate * x, the gate's gradient w * x, of Q columns
+    auto finish = [&](int c, const float (&x)[Q]) {
+      float o[Q];
 #pragma unroll
-        for (int j = 0; j < Q; ++j)
-          a.part_g[(long long)here.unit * d + c + j] = s[i][q + j];
+      for (int j = 0; j < Q; ++j) {
+        acc[c + j] = fmaf(Elem<E>::get(gate[c + j]), x[j], acc[c + j]);
+        o[j] = Elem<E>::get(w[c + j]) * x[j];
+      }
+      E* to = static_cast<E*>(a.dgate) + (long long)k * d + c;
+#pragma unroll
+      for (int j = 0; j < Q; ++j) to[j] = Elem<E>::put(o[j]);
+    };
+    if (!a.alone) {
+      join(false, [&](int c, const float (&x)[Q]) {
+        if (keep) finish(c, x);
+        else store_vec<float, Q>(a.part_g + (long long)here.unit * d + c, x);
       });
-      continue;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (tid + i * a.tpr) * V;
-      if (c < d) {
-        Raw<E, V> x, g;
-        x.load(w + c);
-        g.load(gate + c);
-        float o[V];
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (tid + i * a.tpr) * V;
+        if (c < d)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          acc[c + j] = fmaf(g.get(j), s[i][j], acc[c + j]);
-          o[j] = x.get(j) * s[i][j];
-        }
-        store_vec<E, V>(static_cast<E*>(a.dgate) + (long long)k * d + c, o);
+          for (int q = 0; q < V; q += Q)
+            finish(c + q, *reinterpret_cast<const float(*)[Q]>(&s[i][q]));
       }
     }
   }
   if (GATE && !keep) return;
-  if (!GATE) join();
-  else if (a.alone) __syncthreads();
-  if (mine != 0) return;
-  columns([&](int c, int i, int q) {
-#pragma unroll
-    for (int j = 0; j < Q; ++j) {
-      float x = GATE ? acc[c + j] : s[i][q + j];
-      if (GATE && a.alone)
-        for (int g = 1; g < rows_here; ++g) x += joined[g * d + c + j];
-      a.part_w[(long long)blockIdx.x * d + c + j] = x;
-    }
-  });
+  auto write = [&](int c, const float (&x)[Q]) {
+    store_vec<float, Q>(a.part_w + (long long)blockIdx.x * d + c, x);
+  };
+  if (GATE && !a.alone) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < d; c += blockDim.x)
+      a.part_w[(long long)blockIdx.x * d + c] = acc[c];
+  } else {
+    join(GATE, write);
+  }
 }
 
 // Rows too long for the registers of a block (see norm_shape): the same sums
@@ -678,12 +703,13 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_bwd_wide(const BwdArgs a) 
 // those are the units of split gate rows, each times its gate (`gate` given).
 // blockIdx.y = k + 1: the gradient of split gate row k, from its units, times w.
 // A block sums 32 columns with 32 slices of the rows, joined in order.
+constexpr int JOIN_SLICES = 32;
 template <typename E>
-__global__ void __launch_bounds__(1024) k_norm_join(const float* part_w, int n_part, float* dw,
-                                                    const float* part_g, int split, const E* w,
-                                                    const E* gate, E* dgate, int d) {
+__global__ void __launch_bounds__(32 * JOIN_SLICES)
+    k_norm_join(const float* part_w, int n_part, float* dw, const float* part_g, int split,
+                const E* w, const E* gate, E* dgate, int d) {
   grid_dep_sync();
-  __shared__ float s[32][33];
+  __shared__ float s[JOIN_SLICES][32];
   const int c = blockIdx.x * 32 + threadIdx.x;
   const int k = (int)blockIdx.y - 1;
   const float* p = k < 0 ? part_w : part_g + (long long)k * split * d;
@@ -691,22 +717,21 @@ __global__ void __launch_bounds__(1024) k_norm_join(const float* part_w, int n_p
   float v = 0.f;
   if (c < d) {
     if (k < 0 && gate) {
-#pragma unroll 4
-      for (int i = threadIdx.y; i < n; i += 32)
+#pragma unroll 5
+      for (int i = threadIdx.y; i < n; i += JOIN_SLICES)
         v = fmaf(p[(long long)i * d + c], Elem<E>::get(gate[(long long)(i / split) * d + c]), v);
     } else {
-#pragma unroll 4
-      for (int i = threadIdx.y; i < n; i += 32) v += p[(long long)i * d + c];
+#pragma unroll 5
+      for (int i = threadIdx.y; i < n; i += JOIN_SLICES) v += p[(long long)i * d + c];
     }
   }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  v = warp_sum(s[threadIdx.x][threadIdx.y]);
-  const int co = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && co < d) {
-    if (k < 0) dw[co] = v;
-    else dgate[(long long)k * d + co] = Elem<E>::put(v * Elem<E>::get(w[co]));
-  }
+  if (threadIdx.y != 0 || c >= d) return;
+#pragma unroll
+  for (int i = 1; i < JOIN_SLICES; ++i) v += s[i][threadIdx.x];
+  if (k < 0) dw[c] = v;
+  else dgate[(long long)k * d + c] = Elem<E>::put(v * Elem<E>::get(w[c]));
 }
 
 }  // namespace norm

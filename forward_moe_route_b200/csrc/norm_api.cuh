@@ -32,10 +32,11 @@ moe_status norm_dims(const moe_norm_desc* s, NormDims* D) {
 // How a row is held.  Rows of whole 16-byte vectors are read in vectors
 // (V = 8 bf16 or 4 fp32), others in single elements; rows that do not fit take
 // the looping kernels (vpt = 0).
-// Forward: a row of up to 128 vectors belongs to one warp, a longer one to a
-// block with up to `vpt` vectors a thread.
+// Forward: a row of up to 128 vectors belongs to one warp, a longer one to a block, with one vector a thread when there are fewer
+// rows than SMs and latency counts, else with two or four.
 // Backward: up to 4 vectors (16 single elements) a thread and as many rows a
 // block as it holds.
+constexpr int64_t NORM_SMS = 148;
 struct NormShape {
   int v, vpt, tpr, threads;
   int rows_here() const { return threads / tpr; }
@@ -64,7 +65,7 @@ NormShape norm_shape(const NormDims& D, bool backward) {
     return s;
   }
   const int widest = whole ? 4 : 8;
-  s.vpt = whole ? 2 : 8;
+  s.vpt = !whole ? 8 : D.T < NORM_SMS && n <= norm::MAX_THREADS ? 1 : 2;
   if (n > (int64_t)s.vpt * norm::MAX_THREADS) s.vpt = widest;
   if (n > (int64_t)s.vpt * norm::MAX_THREADS) {
     s.vpt = 0;
@@ -81,7 +82,6 @@ NormShape norm_shape(const NormDims& D, bool backward) {
 // kernel).  A gate row of more tokens
 // is split; gate rows of fewer tokens than keep a block's row groups busy are
 // single row groups' units (`alone`).
-constexpr int64_t NORM_SMS = 148;
 struct NormCut {
   int64_t group, rows, split, units, blocks;
   bool alone;
@@ -130,7 +130,7 @@ constexpr int64_t kNormRing = 8;
 // sums of the row groups, and the weight's when blocks share whole gate rows
 int64_t norm_joined(const NormDims& D, const NormShape& s, const NormCut& c, bool gate) {
   const int64_t keep = gate && c.split == 1 && !c.alone ? 1 : 0;
-  return ((s.rows_here() > 1 ? s.rows_here() : 0) + keep) * D.d * 4;
+  return (s.rows_here() + keep) * D.d * 4;
 }
 int norm_stages(const NormDims& D, const NormShape& s, int parts, int64_t joined) {
   if (s.v == 1) return 1;
@@ -164,7 +164,11 @@ moe_status launch_norm_fwd(const NormShape& s, norm::FwdArgs a, int sms, cudaStr
                          : norm::k_norm_fwd_wide<E, VEC, COMBINE>;
   a.tpr = s.tpr;
   const int64_t blocks = (a.T + s.rows_here() - 1) / s.rows_here();
-  const int64_t most = (int64_t)sms * (2048 / s.threads);
+  // Resident blocks stride over many rows (16384 rows of 7168: 554 us, one block
+  // a row 703 us); with few waves one block a row spares the half-empty last one
+  // (4097 rows of 1001: 7.5 us, strided 9.0 us).
+  const int64_t resident = (int64_t)sms * (2048 / s.threads);
+  const int64_t most = blocks < 4 * resident ? blocks : resident;
   return launch_chain(COMBINE ? "k_norm_fwd (combine)" : "k_norm_fwd", k,
                       dim3((unsigned)(blocks < most ? blocks : most)), dim3(s.threads), 0, st, a);
 }
@@ -185,9 +189,10 @@ moe_status launch_norm_bwd(const NormDims& D, const NormShape& s, const NormCut&
     size_t smem = 0;
     if (!wide) {
       const int parts = a.add ? 3 : 2;
-      smem = (size_t)norm_joined(D, s, c, GATE);
-      a.stages = norm_stages(D, s, parts, (int64_t)smem);
-      if (s.v > 1) smem += (size_t)s.rows_here() * a.stages * parts * a.d * sizeof(E);
+      const size_t joined = (size_t)norm_joined(D, s, c, GATE);
+      a.stages = norm_stages(D, s, parts, GATE ? (int64_t)joined : 0);
+      smem = s.v > 1 ? (size_t)s.rows_here() * a.stages * parts * a.d * sizeof(E) : 0;
+      smem = GATE ? smem + joined : smem > joined ? smem : joined;
       const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)kNormSmem);
       if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (k_norm_bwd)");
@@ -201,7 +206,8 @@ moe_status launch_norm_bwd(const NormDims& D, const NormShape& s, const NormCut&
   // keeps the weight's by themselves)
   const bool shared = gates && !wide;
   return launch_chain("k_norm_join", norm::k_norm_join<E>,
-                      dim3((unsigned)((a.d + 31) / 32), (unsigned)(1 + gates)), dim3(32, 32), 0,
+                      dim3((unsigned)((a.d + 31) / 32), (unsigned)(1 + gates)),
+                      dim3(32, norm::JOIN_SLICES), 0,
                       st, static_cast<const float*>(shared ? a.part_g : a.part_w),
                       (int)(shared ? c.units : c.blocks), dw,
                       static_cast<const float*>(a.part_g), (int)c.split,
