@@ -250,6 +250,151 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_fwd(const FwdArgs a) {
   }
 }
 
+// moe_combine_norm of many tokens whose rows are whole vectors.  The S expert rows
+// and the residual's row of token after token stream through a ring in shared
+// memory, one row a stage: a warp of its own issues the bulk copies, so loads go on
+// while the other warps are at a token's sums and outputs.  Arithmetic as in
+// k_norm_fwd; w and w_next stay in registers.
+constexpr int STREAM_STAGES = 16;      // at most
+template <typename E, int VPT>
+__global__ void __launch_bounds__(VPT == 4 ? 544 : MAX_THREADS) k_combine_stream(const FwdArgs a, int stages) {
+  constexpr int V = Elem<E>::VEC;
+  grid_dep_sync();
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ float red[2][32];
+  __shared__ uint64_t full[STREAM_STAGES], empty[STREAM_STAGES];
+  __shared__ int abort_word;
+  const int tid = (int)threadIdx.x, d = a.d, S = a.S;
+  const int nw = a.tpr >> 5;                       // warps at the rows; one more copies
+  const uint32_t row_bytes = (uint32_t)d * sizeof(E);
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], nw);
+    }
+    abort_word = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  int stage = 0;
+  uint32_t phase = 0;
+  auto advance = [&]() {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  };
+  if (tid >= a.tpr) {
+    if (elect_one()) {
+      bool ok = true;
+      for (long long t = blockIdx.x; t < a.T && ok; t += gridDim.x)
+        for (int s = 0; s <= S && ok; ++s) {
+          ok = mbar_wait(&empty[stage], phase ^ 1u, &abort_word);
+          if (!ok) break;
+          const E* row = s < S ? static_cast<const E*>(a.slots) + (t * S + s) * d
+                               : static_cast<const E*>(a.u) + t * d;
+          mbar_arrive_expect_tx(&full[stage], row_bytes);
+          bulk_load_1d(dyn + (size_t)stage * row_bytes, row, row_bytes, &full[stage]);
+          advance();
+        }
+    }
+    return;
+  }
+  int buf = 0;
+  auto sum = [&](float x) {
+    x = warp_sum(x);
+    if (lane_id() == 0) red[buf][warp_id()] = x;
+    asm volatile("bar.sync 1, %0;" ::"r"(a.tpr) : "memory");
+    x = lane_id() < nw ? red[buf][lane_id()] : 0.f;
+    buf ^= 1;
+    return warp_sum(x);
+  };
+  Raw<E, V> w[VPT], w_next[VPT], gate[VPT], x[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (tid + i * a.tpr) * V;
+    if (c < d) {
+      w[i].load(static_cast<const E*>(a.w) + c);
+      if (a.w_next) w_next[i].load(static_cast<const E*>(a.w_next) + c);
+    }
+  }
+  // the next row of the ring into x (a wait that ran out is reported, and the
+  // results are void)
+  auto take = [&]() {
+    mbar_wait(&full[stage], phase, &abort_word);
+    const E* row = reinterpret_cast<const E*>(dyn + (size_t)stage * row_bytes);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (tid + i * a.tpr) * V;
+      if (c < d) x[i].load(row + c);
+      else x[i].zero();
+    }
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(&empty[stage]);
+    advance();
+  };
+  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+    if (a.gate) {
+      const E* g = static_cast<const E*>(a.gate) + (long long)((int)t / a.gate_group) * d;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (tid + i * a.tpr) * V;
+        if (c < d) gate[i].load(g + c);
+      }
+    }
+    float v[VPT][V];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[i][j] = 0.f;
+    for (int s = 0; s < S; ++s) {
+      take();
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] += x[i].get(j);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (tid + i * a.tpr) * V;
+      if (a.y && c < d) store_vec<E, V>(static_cast<E*>(a.y) + t * d + c, v[i]);
+#pragma unroll
+      for (int j = 0; j < V; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    }
+    const float r = inv_rms(sum(ss), d, a.eps);
+    take();
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (tid + i * a.tpr) * V;
+      if (c < d) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          v[i][j] = v[i][j] * r * w[i].get(j);
+          if (a.gate) v[i][j] *= gate[i].get(j);
+          v[i][j] = fmaf(a.res, x[i].get(j), v[i][j]);
+          ss = fmaf(v[i][j], v[i][j], ss);
+        }
+        store_vec<E, V>(static_cast<E*>(a.h) + t * d + c, v[i]);
+      }
+    }
+    if (a.w_next) {
+      const float rn = inv_rms(sum(ss), d, a.eps);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (tid + i * a.tpr) * V;
+        if (c < d) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[i][j] = v[i][j] * rn * w_next[i].get(j);
+          store_vec<E, V>(static_cast<E*>(a.x_next) + t * d + c, v[i]);
+        }
+      }
+    }
+  }
+}
+
 struct BwdArgs {
   const void* v;         // [T, d]: the normalised rows' input (u before the layer, y behind it)
   const void* w;         // [d]

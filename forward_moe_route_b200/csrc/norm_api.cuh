@@ -123,9 +123,9 @@ NormCut norm_cut(const NormDims& D, int64_t gate_group, const NormShape& s) {
   return c;
 }
 
+constexpr int64_t kNormSmem = 208 * 1024;   // of a block that has an SM to itself
 // Rows in flight for each row group, in the shared memory beside the row groups'
 // sums.
-constexpr int64_t kNormSmem = 208 * 1024;
 constexpr int64_t kNormRing = 8;
 // sums of the row groups, and the weight's when blocks share whole gate rows
 int64_t norm_joined(const NormDims& D, const NormShape& s, const NormCut& c, bool gate) {
@@ -151,6 +151,32 @@ NormLayout norm_layout(const NormDims& D, const NormCut& c, bool wide) {
   L.total = align_up(L.part_g + g * row, kAlign);
   if (!L.total) L.total = kAlign;
   return L;
+}
+
+// Streams many tokens' rows through shared memory: vectors of up to 4 a thread,
+// as many blocks on an SM as 1024 threads hold, the shared memory divided among
+// them.  Short rows stay with k_norm_fwd's warps.
+constexpr int64_t kStreamRow = 2048;      // bytes of a row
+constexpr int64_t kStreamTokens = 592;
+template <typename E>
+moe_status launch_combine_stream(norm::FwdArgs a, int sms, cudaStream_t st) {
+  const int n = a.d / norm::Elem<E>::VEC;
+  const int vpt = n <= 512 ? 1 : n <= 1024 ? 2 : 4;
+  a.tpr = ((n + vpt - 1) / vpt + 31) / 32 * 32;
+  const int threads = a.tpr + 32;
+  const int per_sm = 1024 / threads < 1 ? 1 : 1024 / threads > 4 ? 4 : 1024 / threads;
+  const int64_t row = (int64_t)a.d * sizeof(E);
+  int stages = (int)(kNormSmem / per_sm / row);
+  if (stages > norm::STREAM_STAGES) stages = norm::STREAM_STAGES;
+  auto* k = vpt == 1   ? norm::k_combine_stream<E, 1>
+            : vpt == 2 ? norm::k_combine_stream<E, 2>
+                       : norm::k_combine_stream<E, 4>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)kNormSmem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (k_combine_stream)");
+  const int64_t blocks = a.T < (int64_t)sms * per_sm ? a.T : (int64_t)sms * per_sm;
+  return launch_chain("k_combine_stream", k, dim3((unsigned)blocks), dim3(threads),
+                      (size_t)stages * row, st, a, stages);
 }
 
 template <typename E, bool COMBINE>
@@ -302,6 +328,10 @@ moe_status moe_combine_norm(const moe_norm_desc* desc, const void* x_residual,
   a.h = h; a.y = y; a.x_next = x_next;
   a.T = (int)D.T; a.d = (int)D.d; a.S = desc->n_slots; a.gate_group = desc->gate_group;
   a.eps = desc->eps; a.res = desc->res_scale;
+  if (D.d % D.vec == 0 && D.d * (D.bf16 ? 2 : 4) >= kStreamRow && D.d / D.vec <= 2048 &&
+      D.T >= kStreamTokens)
+    return D.bf16 ? launch_combine_stream<__nv_bfloat16>(a, sms, stream)
+                  : launch_combine_stream<float>(a, sms, stream);
   const NormShape s = norm_shape(D, false);
   return D.bf16 ? launch_norm_fwd<__nv_bfloat16, true>(s, a, sms, stream)
                 : launch_norm_fwd<float, true>(s, a, sms, stream);

@@ -216,3 +216,36 @@ def test_graph_and_side_stream():
     torch.cuda.synchronize()
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+# many tokens: rows of 128 vectors, one, two and four vectors a thread, a last thread without any
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [1024, 1032, 2056, 5120, 8192])
+@pytest.mark.parametrize("slots,gate_group", [(1, 0), (9, 700), (2, 1)])
+def test_combine_norm_of_many_tokens(d, slots, gate_group, dtype):
+    gen = torch.Generator(device="cuda").manual_seed(d + slots)
+    T = 1301 if d < 4000 else 593
+
+    def draw(*shape, std=1.0, mean=0.0):
+        x = torch.randn(*shape, generator=gen, device="cuda") * std + mean
+        return x.to(TYPES[dtype])
+
+    u, ys = draw(T, d, std=2.0), draw(T, slots, d)
+    w, wn = draw(d, mean=1.0, std=0.2), draw(d, mean=1.0, std=0.2)
+    gate = draw(-(-T // gate_group), d, mean=0.5, std=0.3) if gate_group else None
+    desc = moe.make_norm_desc(T, d, EPS, dtype, slots, gate_group, 0.75)
+    h, y, x_next = (torch.full_like(u, float("nan")) for _ in range(3))
+    moe.moe_combine_norm(desc, u, ys, w, gate, wn, h, y, x_next)
+    wh, wy, wx = block.combine_norm(f64(u), f64(ys), f64(w), f64(gate), gate_group, 0.75, f64(wn),
+                                    desc.eps)
+    g = block.gate_rows(f64(gate), gate_group, T)
+    ymag = np.abs(f64(ys)).sum(1)
+    hmag = np.abs(0.75 * f64(u)) + np.abs(g * f64(w)) * ymag * block.inv_rms(wy, desc.eps)
+    close("y", y, wy, ymag, dtype)
+    close("h", h, wh, hmag, dtype)
+    close("x_next", x_next, wx, np.abs(f64(wn)) * block.inv_rms(wh, desc.eps) *
+          (hmag + np.abs(wh)), dtype)
+    again = torch.full_like(h, float("nan"))
+    moe.moe_combine_norm(desc, u, ys, w, gate, None, again, None, None)
+    assert torch.equal(again, h)
+    assert moe.moe_last_device_status() == moe.OK
