@@ -15,18 +15,25 @@ namespace {
 constexpr int kMaxTensors = 1 << 24;    // the random counter has 24 bits for the tensor
 constexpr int64_t kMaxChunks = 0x7fffffff;
 
-int64_t adamw_chunks(int64_t n, bool small) {
-  const int64_t size = small ? adamw::CHUNK8 : adamw::CHUNK;
+// Spans of a chunk: with 8-bit states a block asks for spans while it works on the
+// ones before, so chunks are as long as four blocks of them on each of 148 SMs
+// still come in four waves, 16 at most.  fp32 states are bound by memory with one.
+int adamw_spans(int64_t elements, bool small) {
+  const int64_t n = small ? elements / ((int64_t)adamw::SPAN * 148 * 16) : 1;
+  return n < 1 ? 1 : n > 16 ? 16 : (int)n;
+}
+int64_t adamw_chunks(int64_t n, int spans) {
+  const int64_t size = (int64_t)spans * adamw::SPAN;
   return n / size + (n % size != 0);
 }
 
-// total chunks of the list, -1 when a length or the count is not accepted
+// chunks of one span of the list, -1 when a length or the count is not accepted
 int64_t adamw_list_chunks(const moe_adamw_tensor* tensors, int32_t n) {
   if (n < 0 || n > kMaxTensors || (n > 0 && !tensors)) return -1;
   int64_t chunks = 0;
   for (int32_t i = 0; i < n; ++i) {
     if (tensors[i].n < 0) return -1;
-    const int64_t c = adamw_chunks(tensors[i].n, false);   // the larger count of the two
+    const int64_t c = adamw_chunks(tensors[i].n, 1);
     if (c > kMaxChunks - chunks) return -1;
     chunks += c;
   }
@@ -70,6 +77,7 @@ moe_status moe_adamw_table(const moe_adamw_tensor* tensors, int32_t n_tensors, i
   memset(image, 0, table_bytes);
   int32_t* map = reinterpret_cast<int32_t*>(image + adamw_map_at(n_tensors));
   int64_t chunk = 0;
+  const int per_chunk = adamw_spans(chunks * adamw::SPAN, small);
   for (int32_t i = 0; i < n_tensors; ++i) {
     const moe_adamw_tensor& s = tensors[i];
     if (s.n == 0) continue;
@@ -84,8 +92,8 @@ moe_status moe_adamw_table(const moe_adamw_tensor* tensors, int32_t n_tensors, i
       bool written;
     } parts[7] = {{s.p, n * 4, 4, 32, true},
                   {s.grad, n * gsz, gsz, gsz * 8, false},
-                  {s.m, n * state, state, state * 8, true},
-                  {s.v, n * state, state, state * 8, true},
+                  {s.m, n * state, state, small ? 16u : 32u, true},
+                  {s.v, n * state, state, small ? 16u : 32u, true},
                   {small ? s.m_scale : nullptr, scales, 4, 4, true},
                   {small ? s.v_scale : nullptr, scales, 4, 4, true},
                   {s.p_bf16, n * 2, 2, 16, true}};
@@ -109,8 +117,9 @@ moe_status moe_adamw_table(const moe_adamw_tensor* tensors, int32_t n_tensors, i
     e.n = s.n;
     e.first = (int)chunk;
     e.decay = s.weight_decay;
+    e.spans = per_chunk;
     memcpy(image + (size_t)i * sizeof(e), &e, sizeof(e));
-    for (int64_t c = adamw_chunks(s.n, small); c > 0; --c) map[chunk++] = i;
+    for (int64_t c = adamw_chunks(s.n, per_chunk); c > 0; --c) map[chunk++] = i;
   }
   // nothing that is written may be any other tensor's, or another part of the same
   std::sort(spans.begin(), spans.end());
@@ -161,7 +170,13 @@ moe_status moe_adamw(const moe_adamw_desc* desc, const void* table, int32_t n_te
   auto* k = desc->state_bits == 8
                 ? (dev ? adamw::k_adamw<true, true> : adamw::k_adamw<true, false>)
                 : (dev ? adamw::k_adamw<false, true> : adamw::k_adamw<false, false>);
-  return launch_chain("k_adamw", k, dim3((unsigned)n_chunks), dim3(adamw::THREADS), 0, stream, a);
+  const size_t smem = desc->state_bits == 8 ? adamw::RING_BYTES : 0;
+  if (smem) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (k_adamw)");
+  }
+  return launch_chain("k_adamw", k, dim3((unsigned)n_chunks), dim3(adamw::THREADS), smem, stream, a);
 }
 
 }  // extern "C"

@@ -618,8 +618,8 @@ typedef struct moe_adamw_tensor {
  * pointer; `tensors` is a host array of device pointers).  n_chunks: what
  * moe_adamw takes.  Refused: memory that two tensors of the list, or two parts
  * of one, would both write.  Addresses only need their element's alignment;
- * tensors whose p, m, v (fp32) are 32-byte, grad 8-element, bf16 copy 16-byte
- * and codes 8-byte aligned run fastest.  At most 2^24 tensors. */
+ * tensors whose p, fp32 m and v are 32-byte, grad 8-element, bf16 copy and codes
+ * 16-byte aligned run fastest.  At most 2^24 tensors. */
 size_t moe_adamw_table_size(const moe_adamw_tensor* tensors, int32_t n_tensors);
 moe_status moe_adamw_table(const moe_adamw_tensor* tensors, int32_t n_tensors, int32_t state_bits,
                            void* table, size_t table_bytes, int64_t* n_chunks);
