@@ -891,13 +891,13 @@ def adamw_table(p, grad, m, v, p_bf16=None, weight_decay=0.0, m_scale=None,
                  weight_decay=decay)
     for name, items in lists.items():
         if items is None or len(items) != n:
-            raise MoeError(ERR_INVALID_ARG, f"{where}: {name} is not a list of {n}")
+            _refuse(where, f"{name} is not a list of {n}")
     array = (MoeAdamwTensor * n)()
     held = []
     for i in range(n):
         t = {k: x[i] for k, x in lists.items()}
         if t["p"] is None:
-            raise MoeError(ERR_INVALID_ARG, f"{where}: p[{i}] is missing")
+            _refuse(where, f"p[{i}] is missing")
         size = t["p"].numel()
         blocks = -(-size // 128)
         wanted = [("p", size, _F32), ("grad", size, ("float32", "bfloat16")),
@@ -914,7 +914,7 @@ def adamw_table(p, grad, m, v, p_bf16=None, weight_decay=0.0, m_scale=None,
         array[i] = MoeAdamwTensor(*at, size, t["weight_decay"], int(t["grad"].element_size() == 2))
     bytes_ = int(_lib.moe_adamw_table_size(array, n))
     if bytes_ == 0:
-        raise MoeError(ERR_INVALID_ARG, f"{where}: too many tensors or elements")
+        _refuse(where, "too many tensors or elements")
     image = torch.empty(bytes_, dtype=torch.uint8)
     chunks = ctypes.c_int64()
     _check(_lib.moe_adamw_table(array, n, bits, image.data_ptr(), bytes_, ctypes.byref(chunks)),
@@ -926,8 +926,10 @@ def moe_adamw(desc, table: AdamwTable, step, lr=None, stream=None) -> None:
     """One AdamW step over the table's tensors.  step: an int >= 1, or a CUDA int32 tensor of one
     element that the kernel reads; lr: None (desc.lr) or a CUDA float32 tensor of one element."""
     if table.state_bits != desc.state_bits:
-        raise MoeError(ERR_INVALID_ARG, f"moe_adamw: a table of {table.state_bits}-bit states")
+        _refuse("moe_adamw", f"a table of {table.state_bits}-bit states")
     on_device = not isinstance(step, int)
+    if not on_device and not 1 <= step < 2 ** 31:
+        _refuse("moe_adamw", f"step {step} is not within 1..2^31 - 1")
     at = _operands("moe_adamw", (("table", table.table, 0, _U8, False),
                                  ("step", step if on_device else None, 1, _I32, not on_device),
                                  ("lr", lr, 1, _F32, True)))

@@ -396,8 +396,8 @@ __device__ __forceinline__ void step_chunk(const Args& a, const Coef& c, const E
   for (int i = 0; i < e.spans && first + (long long)i * SPAN < e.n; ++i) {
     const long long at = mine + (long long)i * SPAN;
     if constexpr (RING) {
-      // a wait that ran out is reported, and the span's results are void
-      mbar_wait(&full[i % STAGES], (uint32_t)(i / STAGES) & 1u, abort);
+      // a wait that ran out is reported, and the rest of the chunk left as it is
+      const bool there = mbar_wait(&full[i % STAGES], (uint32_t)(i / STAGES) & 1u, abort);
       held.load_span(ring + (i % STAGES) * BYTES);
       held.m_scale = m_scale;
       held.v_scale = v_scale;
@@ -405,7 +405,7 @@ __device__ __forceinline__ void step_chunk(const Args& a, const Coef& c, const E
         m_scale = e.m_scale[(at + SPAN) / BLOCK];
         v_scale = e.v_scale[(at + SPAN) / BLOCK];
       }
-      __syncthreads();                       // the span is in registers
+      if (!__syncthreads_and(there)) return;   // the span is in registers
       if (threadIdx.x == 0 && i + STAGES < e.spans) fetch(i + STAGES);
     } else {
       held.load(e, at);

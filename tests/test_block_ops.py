@@ -309,5 +309,8 @@ def test_adamw_binding_refuses():
         with pytest.raises(moe.MoeError, match=what) as err:
             moe.adamw_table(**{**dict(p=[f], grad=[f], m=[f], v=[f]), **kw})
         assert err.value.status == moe.ERR_INVALID_ARG
+    for step in (0, -1, 2 ** 31, 2 ** 32 + 1):
+        with pytest.raises(moe.MoeError, match="step"):
+            moe.moe_adamw(moe.make_adamw_desc(1e-3), moe.AdamwTable(None, 0, 0, 32, []), step)
     with pytest.raises(moe.MoeError, match="8-bit"):
         moe.moe_adamw(moe.make_adamw_desc(1e-3), moe.AdamwTable(None, 0, 0, 8, []), 1)

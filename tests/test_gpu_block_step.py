@@ -203,3 +203,23 @@ def test_captured_steps_repeat_eager_ones(bits):
         assert a.float().isfinite().all() if a.is_floating_point() else True
         assert torch.equal(a, b)
     assert moe.moe_last_device_status() == moe.OK
+
+
+def test_two_blocks_on_two_streams():
+    alone = [Block(32, seed=3), Block(8, seed=4)]
+    for m in alone:
+        for _ in range(4):
+            m.step()
+    torch.cuda.synchronize()
+    both = [Block(32, seed=3), Block(8, seed=4)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in both]
+    for _ in range(4):
+        for m, s in zip(both, streams):
+            with torch.cuda.stream(s):
+                m.step()
+    torch.cuda.synchronize()
+    for m, n in zip(alone, both):
+        for a, b in zip(m.tensors(), n.tensors()):
+            assert torch.equal(a, b)
+    assert moe.moe_last_device_status() == moe.OK
