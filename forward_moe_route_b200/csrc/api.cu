@@ -119,9 +119,10 @@ struct DeviceInfo {
   // co-resident 2-CTA clusters of the pair GEMMs (0: gate/up, 1: down,
   // 2: backward weight gradients, 3: backward activation GEMMs, 4 and 5:
   // grouped products and their row gradients, 6 and 7: their weight gradients
-  // in fp32 and bf16), and the dynamic shared memory each count was taken for
-  size_t pair_smem[8] = {};
-  int pair_clusters[8] = {};
+  // in fp32 and bf16, 8: the products of groups of few rows), and the dynamic
+  // shared memory each count was taken for
+  size_t pair_smem[9] = {};
+  int pair_clusters[9] = {};
 };
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
@@ -180,10 +181,13 @@ moe_status device_setup(int* sms) {
       e = cudaFuncSetAttribute(gemm8::k_gemm_promoted<2, gemm8::EPI_BF16_OUT, true>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(grouped::k_grouped_mm<false>,
+      e = cudaFuncSetAttribute(grouped::k_grouped_mm<false, grouped::TILE_ROWS>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(grouped::k_grouped_mm<true>,
+      e = cudaFuncSetAttribute(grouped::k_grouped_mm<false, grouped::FEW_ROWS>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(grouped::k_grouped_mm<true, grouped::TILE_ROWS>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(grouped::k_grouped_dw<false>,

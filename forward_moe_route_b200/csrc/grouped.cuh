@@ -60,8 +60,19 @@ constexpr uint32_t TAB_BYTES = (3 * MAX_GROUPS + 1) * 4 + 12;
 constexpr int MM_THREADS = 384;
 constexpr int MM_EPI_WARPS = 8;
 constexpr uint32_t MM_XPOSE = 16 * 32 * 2;     // a warp's 16 rows x 32 features, bf16
-constexpr uint32_t MM_SMEM = 1024 + STAGES * STAGE_BYTES + MM_EPI_WARPS * MM_XPOSE + BAR_BYTES +
-                             TAB_BYTES;
+// Row tiles of up to 256 rows, or of up to FEW_ROWS where groups are so small that
+// the weights set the pace: a stage then keeps less for the rows, and ten of them
+// instead of six hold more of the weight stream in flight.
+constexpr int TILE_ROWS = 256;
+constexpr int FEW_ROWS = 64;
+__host__ __device__ constexpr int mm_stages(int tile_rows) { return tile_rows == FEW_ROWS ? 10 : STAGES; }
+__host__ __device__ constexpr uint32_t mm_stage_bytes(int tile_rows) {
+  return HALF_STAGE + tile_rows / 2 * 128;
+}
+constexpr uint32_t mm_smem(int tile_rows) {
+  return 1024 + mm_stages(tile_rows) * mm_stage_bytes(tile_rows) + MM_EPI_WARPS * MM_XPOSE +
+         (2 * mm_stages(tile_rows) + 6) * 8 + 16 + TAB_BYTES;
+}
 
 // ---- weight gradients -----------------------------------------------------------------
 constexpr int DW_THREADS = 384;
@@ -71,7 +82,8 @@ constexpr int DW_EPI_WARPS = 8;
 constexpr uint32_t DW_STAGING = 4096;
 constexpr uint32_t DW_STORE = DW_EPI_WARPS * DW_STAGING;
 constexpr uint32_t DW_SMEM = 1024 + STAGES * STAGE_BYTES + DW_STORE + BAR_BYTES;
-static_assert(MM_SMEM <= 232448 && DW_SMEM <= 232448, "shared memory of one block");
+static_assert(mm_smem(TILE_ROWS) <= 232448 && mm_smem(FEW_ROWS) <= 232448 && DW_SMEM <= 232448,
+              "shared memory of one block");
 
 struct Args {
   const int* offsets;   // [n + 1]
@@ -104,19 +116,23 @@ __device__ __forceinline__ bool group_ok(int r0, int r1, int n_rows) {
   return r0 >= 0 && r1 >= r0 && r1 <= n_rows;
 }
 
-// k_grouped_mm cuts a group of r rows into ceil(r / 256) row tiles of equal
+// k_grouped_mm cuts a group of r rows into ceil(r / ROWS) row tiles of equal
 // height, rounded up to the 32 rows that the UMMA N goes by (r = 257: 160 + 97,
 // not 256 + 1): 5 to 8% faster than full tiles and a rest on uneven groups, as
 // a low tile costs the loads of its weights all the same.
-constexpr int TILE_ROWS = 256;
-__device__ __forceinline__ int row_tiles(int rows) { return (rows + TILE_ROWS - 1) / TILE_ROWS; }
+template <int ROWS>
+__device__ __forceinline__ int row_tiles(int rows) {
+  return (rows + ROWS - 1) / ROWS;
+}
+template <int ROWS>
 __device__ __forceinline__ int tile_height(int rows) {
-  const int n = row_tiles(rows);
+  const int n = row_tiles<ROWS>(rows);
   return n ? ((rows + n - 1) / n + 31) & ~31 : 0;
 }
 
 // The group list in shared memory: first row and rows of each group, and the
 // prefix of its row tiles.  One warp builds it.
+template <int ROWS>
 struct Groups {
   int *row0, *rows, *prefix;   // [n], [n], [n + 1]
   int n;
@@ -135,7 +151,7 @@ struct Groups {
         row0[g] = r0;
         rows[g] = r;
       }
-      const int v = row_tiles(r);
+      const int v = row_tiles<ROWS>(r);
       int incl = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -149,19 +165,20 @@ struct Groups {
   }
 };
 
-template <bool W_MN>
+template <bool W_MN, int ROWS>
 __global__ void __launch_bounds__(MM_THREADS, 1)
     k_grouped_mm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                  const __grid_constant__ CUtensorMap tmX64,
                  const __grid_constant__ CUtensorMap tmX32, const Args a) {
   using namespace gemmt;   // cluster helpers of the pair kernels
   constexpr int TF = 256;             // features of a pair's tile
-  constexpr int S = STAGES;
+  constexpr int S = mm_stages(ROWS);
+  constexpr uint32_t SB = mm_stage_bytes(ROWS);
   grid_dep_sync();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* xpose = smem + S * STAGE_BYTES;
+  uint8_t* xpose = smem + S * SB;
   uint64_t* full = reinterpret_cast<uint64_t*>(xpose + MM_EPI_WARPS * MM_XPOSE);
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;
@@ -169,7 +186,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  Groups gr(reinterpret_cast<int*>(tmem_slot + 4), a.n);
+  Groups<ROWS> gr(reinterpret_cast<int*>(tmem_slot + 4), a.n);
 
   const int warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_rank();
@@ -219,7 +236,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     const int rt = tile / n_ft;
     t.ft = tile - rt * n_ft;
     const int p = gemm::find_group(gr.prefix, a.n, rt);
-    const int height = tile_height(gr.rows[p]), at = (rt - gr.prefix[p]) * height;
+    const int height = tile_height<ROWS>(gr.rows[p]), at = (rt - gr.prefix[p]) * height;
     t.g = p;
     t.row = gr.row0[p] + at;
     t.rows = min(height, gr.rows[p] - at);
@@ -244,7 +261,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
           const int s = it % S;
           const uint32_t ph = (uint32_t)(it / S) & 1u;
           if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag)) { ok = false; break; }
-          uint8_t* sw = smem + (size_t)s * STAGE_BYTES;
+          uint8_t* sw = smem + (size_t)s * SB;
           const uint32_t fl = mapa(smem_u32(&full[s]), 0);
           if (leader) mbar_arrive_expect_tx(&full[s], 2 * bytes);
           const int k = kb * 64;
@@ -255,10 +272,10 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             tma_load_3d_pair(&tmW, fl, sw, k, f, t.g);
           }
           uint8_t* sx = sw + HALF_STAGE;
-          if (load == 128) {
+          if (ROWS == TILE_ROWS && load == 128) {
             tma_load_2d_pair(&tmX, fl, sx, k, xrow);
           } else {
-            if (load & 64) tma_load_2d_pair(&tmX64, fl, sx, k, xrow);
+            if (ROWS == TILE_ROWS && (load & 64)) tma_load_2d_pair(&tmX64, fl, sx, k, xrow);
             if (load & 32)
               tma_load_2d_pair(&tmX32, fl, sx + (load & 64) * 128, k, xrow + (load & 64));
           }
@@ -288,7 +305,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
           const uint32_t ph = (uint32_t)(it / S) & 1u;
           if (!mbar_wait(&full[s], ph, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sw = smem_u32(smem + (size_t)s * STAGE_BYTES);
+          const uint32_t sw = smem_u32(smem + (size_t)s * SB);
           const uint64_t wd = W_MN ? gbwd::umma_desc_sw128_mn(sw) : umma_desc_sw128(sw);
           const uint64_t xd = umma_desc_sw128(sw + HALF_STAGE);
           constexpr uint64_t w_step = W_MN ? (2048 >> 4) : (32 >> 4);

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "grouped.cuh"
+#include "grouped_few.cuh"
 
 namespace {
 
@@ -40,11 +41,41 @@ moe_status grouped_dims(int32_t n_groups, int32_t n_rows, int32_t d_in, int32_t 
   return MOE_OK;
 }
 
+// Products of at most FEW_MAX rows, two a group on average, whose weights are 64 MB
+// at most stream them by k_few_mm (above, the tensor cores' pipeline is as fast or
+// faster: 6 rows in 6 of 64 groups 2048 x 2816, 69 MB, 15.9 and 16.9 us, 16 rows 41
+// and 35 us; 8 rows of one group 4096 x 4096 26 and 16 us).
+constexpr int64_t kFewBytes = 64 << 20;
+bool grouped_few(const grouped::Args& a) {
+  return a.n_rows <= grouped::FEW_MAX && a.n_rows <= 2 * a.n &&
+         2ll * a.n_rows * a.feats * a.contract <= kFewBytes;
+}
+moe_status launch_grouped_few(const grouped::Args& a, const void* x, const void* w, int sms,
+                              cudaStream_t st) {
+  // as many items as there can be, each row with a group of its own
+  const int64_t items = (int64_t)(a.n < a.n_rows ? a.n : a.n_rows) *
+                        ((a.feats + grouped::FEW_FEATURES - 1) / grouped::FEW_FEATURES);
+  const int64_t blocks = (items + grouped::FEW_THREADS / 32 - 1) / (grouped::FEW_THREADS / 32);
+  return launch_chain("k_few_mm", grouped::k_few_mm,
+                      dim3((unsigned)(blocks < 16 * sms ? blocks : 16 * sms)),
+                      dim3(grouped::FEW_THREADS), 0, st, a,
+                      static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(w));
+}
+
 // y = rows x W^T (dx: rows x W); the weights [G, d_out, d_in]
 moe_status launch_grouped_mm(bool dx, int32_t G, int32_t R, int32_t d_in, int32_t d_out,
                              const void* rows, const void* w, const int32_t* offsets, void* y,
-                             cudaStream_t st) {
+                             int sms, cudaStream_t st) {
   const uint64_t contract = dx ? d_out : d_in, feats = dx ? d_in : d_out;
+  grouped::Args a;
+  memset(&a, 0, sizeof(a));
+  a.offsets = offsets;
+  a.n = G;
+  a.n_rows = R;
+  a.feats = (int)feats;
+  a.contract = (int)contract;
+  a.y = static_cast<__nv_bfloat16*>(y);
+  if (!dx && grouped_few(a)) return launch_grouped_few(a, rows, w, sms, st);
   const uint64_t wdims[3] = {(uint64_t)d_in, (uint64_t)d_out, (uint64_t)G};
   const uint32_t wbox[3] = {64, dx ? 64u : 128u, 1};
   const uint64_t xdims[2] = {contract, (uint64_t)R};
@@ -54,21 +85,22 @@ moe_status launch_grouped_mm(bool dx, int32_t G, int32_t R, int32_t d_in, int32_
   for (int i = 0; i < 3 && rc == MOE_OK; ++i)
     rc = grouped_map(&tx[i], rows, false, 2, xdims, xbox[i]);
   if (rc != MOE_OK) return rc;
-  grouped::Args a;
-  memset(&a, 0, sizeof(a));
-  a.offsets = offsets;
-  a.n = G;
-  a.n_rows = R;
-  a.feats = (int)feats;
-  a.contract = (int)contract;
-  a.y = static_cast<__nv_bfloat16*>(y);
+  // Groups of 32 rows on average or fewer take the lower row tiles (64 groups 2048 x
+  // 2816 of 8 rows: 122 and 127 us, of 32 rows 125 and 129 us, of 64 rows no
+  // difference).  The row gradients, whose weights come in whole lines either way,
+  // were slower with them (116 and 110 us).
+  const bool few = !dx && R <= (int64_t)G * 32;
   // at most this many row tiles: every group may add a partly filled one
-  const int64_t row_tiles = R / 256 + (G < R ? G : R);
+  const int64_t row_tiles = R / (few ? grouped::FEW_ROWS : grouped::TILE_ROWS) + (G < R ? G : R);
   const int64_t tiles = row_tiles * (int64_t)((feats + 255) / 256);
-  auto* k = dx ? grouped::k_grouped_mm<true> : grouped::k_grouped_mm<false>;
+  auto* k = dx    ? grouped::k_grouped_mm<true, grouped::TILE_ROWS>
+            : few ? grouped::k_grouped_mm<false, grouped::FEW_ROWS>
+                  : grouped::k_grouped_mm<false, grouped::TILE_ROWS>;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  rc = pair_config(dx ? 5 : 4, k, grouped::MM_THREADS, grouped::MM_SMEM, tiles, st, &cfg, attr);
+  rc = pair_config(dx ? 5 : few ? 8 : 4, k, grouped::MM_THREADS,
+                   few ? grouped::mm_smem(grouped::FEW_ROWS) : grouped::mm_smem(grouped::TILE_ROWS),
+                   tiles, st, &cfg, attr);
   if (rc != MOE_OK) return rc;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k, tw, tx[0], tx[1], tx[2], a);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "k_grouped_mm");
@@ -88,7 +120,7 @@ moe_status moe_grouped_mm(int32_t n_groups, int32_t n_rows, int32_t d_in, int32_
     return MOE_ERR_INVALID_ARG;
   int sms;
   if ((rc = device_setup(&sms)) != MOE_OK) return rc;
-  return launch_grouped_mm(false, n_groups, n_rows, d_in, d_out, x, w, offsets, y, stream);
+  return launch_grouped_mm(false, n_groups, n_rows, d_in, d_out, x, w, offsets, y, sms, stream);
 }
 
 moe_status moe_grouped_mm_dx(int32_t n_groups, int32_t n_rows, int32_t d_in, int32_t d_out,
@@ -101,7 +133,7 @@ moe_status moe_grouped_mm_dx(int32_t n_groups, int32_t n_rows, int32_t d_in, int
     return MOE_ERR_INVALID_ARG;
   int sms;
   if ((rc = device_setup(&sms)) != MOE_OK) return rc;
-  return launch_grouped_mm(true, n_groups, n_rows, d_in, d_out, dy, w, offsets, dx, stream);
+  return launch_grouped_mm(true, n_groups, n_rows, d_in, d_out, dy, w, offsets, dx, sms, stream);
 }
 
 moe_status moe_grouped_mm_dw(int32_t n_groups, int32_t n_rows, int32_t d_in, int32_t d_out,

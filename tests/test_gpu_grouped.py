@@ -187,3 +187,14 @@ def test_graph_follows_the_offsets_and_two_runs_agree():
         for p, q in zip(held, eager):
             assert torch.equal(p, q)
     assert moe.moe_last_device_status() == moe.OK
+
+
+# a handful of rows: alone, in one group, in more than a pass of a group holds, with gaps
+@pytest.mark.parametrize("loads", [[1], [16], [5, 0, 2], [0, 0, 3, 4, 9], [1] * 9, [0] * 40 + [7]],
+                         ids=lambda v: f"{len(v)}g{sum(v)}")
+@pytest.mark.parametrize("d_in,d_out", [(8, 16), (64, 72), (1000, 264), (2048, 24), (40, 2056)])
+def test_a_handful_of_rows(loads, d_in, d_out):
+    gen = torch.Generator().manual_seed(sum(loads) + d_in + d_out)
+    check(gen, loads, d_in, d_out)
+    if sum(loads) < 14:
+        check(gen, loads, d_in, d_out, before=1, behind=1)
