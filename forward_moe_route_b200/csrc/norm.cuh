@@ -81,8 +81,8 @@ struct Raw {
   }
   __device__ __forceinline__ void load(const E* p) {
     if constexpr (V == 1) {
-      word[0] = 0u;
-      *reinterpret_cast<E*>(word) = *p;
+      if constexpr (sizeof(E) == 4) word[0] = *reinterpret_cast<const uint32_t*>(p);
+      else word[0] = *reinterpret_cast<const uint16_t*>(p);
     } else {
       const uint4 x = *reinterpret_cast<const uint4*>(p);
       word[0] = x.x;
@@ -121,6 +121,43 @@ struct RowGroup {
 __device__ __forceinline__ float inv_rms(float sumsq, int d, float eps) {
   return 1.0f / sqrtf(sumsq / (float)d + eps);
 }
+
+// Rows of d elements in shared memory, by bulk copies, which go by 16 bytes.  Rows of
+// whole vectors (V > 1) are copied as they are.  Others (V = 1) start and end inside
+// a 16-byte piece: the pieces that cover the row are copied, its elements then stand
+// `shift` bytes from the copy's start; a piece that reaches behind the array (of
+// `total` elements) is not, its elements are written one by one.
+template <typename E, int V>
+struct SharedRow {
+  static constexpr uint32_t SZ = sizeof(E);
+  __host__ __device__ static constexpr uint32_t room(int d) {
+    return V > 1 ? d * SZ : (d * SZ + 15) / 16 * 16 + 16;
+  }
+  static __device__ __forceinline__ uint32_t shift(long long at) {
+    return V > 1 ? 0u : (uint32_t)(at * SZ) & 15u;
+  }
+  // bytes of the copy of the row that begins with element `at`
+  static __device__ __forceinline__ uint32_t bytes(long long at, int d, long long total) {
+    if (V > 1) return d * SZ;
+    const long long lo = at * SZ & ~15ll;
+    const long long hi = min(((at + d) * SZ + 15) & ~15ll, total * SZ & ~15ll);
+    return hi > lo ? (uint32_t)(hi - lo) : 0u;
+  }
+  // before the arrival that makes the row complete
+  static __device__ __forceinline__ void last_elements(uint8_t* to, const E* array, long long at,
+                                                       int d, long long total) {
+    if (V > 1) return;
+    const long long lo = at * SZ & ~15ll, end = (lo + bytes(at, d, total)) / SZ;
+    for (long long e = end > at ? end : at; e < at + d; ++e)
+      *reinterpret_cast<E*>(to + (e * SZ - lo)) = array[e];
+  }
+  static __device__ __forceinline__ void copy(uint8_t* to, const E* array, long long at, int d,
+                                              long long total, uint64_t* bar) {
+    const uint32_t n = bytes(at, d, total);
+    const long long lo = V > 1 ? at * SZ : at * SZ & ~15ll;
+    if (n) bulk_load_1d(to, reinterpret_cast<const uint8_t*>(array) + lo, n, bar);
+  }
+};
 
 struct FwdArgs {
   const void* u;         // [T, d]: the input of k_norm; the residual of k_combine_norm
@@ -250,23 +287,25 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_fwd(const FwdArgs a) {
   }
 }
 
-// moe_combine_norm of many tokens whose rows are whole vectors.  The S expert rows
-// and the residual's row of token after token stream through a ring in shared
-// memory, one row a stage: a warp of its own issues the bulk copies, so loads go on
-// while the other warps are at a token's sums and outputs.  Arithmetic as in
-// k_norm_fwd; w and w_next stay in registers.
+// moe_combine_norm of many tokens (and moe_norm of rows that are not whole vectors).
+// The S expert rows and the residual's row of token after token stream through a
+// ring in shared memory, one row a stage: a warp of its own issues the copies, so
+// loads go on while the other warps are at a token's sums and outputs.  Arithmetic
+// as in k_norm_fwd; w and w_next stay in registers.
 constexpr int STREAM_STAGES = 16;      // at most
-template <typename E, int VPT>
-__global__ void __launch_bounds__(VPT == 4 ? 544 : MAX_THREADS) k_combine_stream(const FwdArgs a, int stages) {
-  constexpr int V = Elem<E>::VEC;
+template <typename E, int V, int VPT, bool COMBINE>
+__global__ void __launch_bounds__(V > 1 && VPT == 4 ? 544 : MAX_THREADS)
+    k_norm_stream(const FwdArgs a, int stages) {
+  using Row = SharedRow<E, V>;
   grid_dep_sync();
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ float red[2][32];
   __shared__ uint64_t full[STREAM_STAGES], empty[STREAM_STAGES];
   __shared__ int abort_word;
-  const int tid = (int)threadIdx.x, d = a.d, S = a.S;
+  const int tid = (int)threadIdx.x, d = a.d, S = COMBINE ? a.S : 0;
   const int nw = a.tpr >> 5;                       // warps at the rows; one more copies
-  const uint32_t row_bytes = (uint32_t)d * sizeof(E);
+  const uint32_t row_bytes = Row::room(d);
+  const long long rows = a.T;
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
@@ -292,10 +331,12 @@ __global__ void __launch_bounds__(VPT == 4 ? 544 : MAX_THREADS) k_combine_stream
         for (int s = 0; s <= S && ok; ++s) {
           ok = mbar_wait(&empty[stage], phase ^ 1u, &abort_word);
           if (!ok) break;
-          const E* row = s < S ? static_cast<const E*>(a.slots) + (t * S + s) * d
-                               : static_cast<const E*>(a.u) + t * d;
-          mbar_arrive_expect_tx(&full[stage], row_bytes);
-          bulk_load_1d(dyn + (size_t)stage * row_bytes, row, row_bytes, &full[stage]);
+          const E* array = static_cast<const E*>(s < S ? a.slots : a.u);
+          const long long at = (s < S ? t * S + s : t) * d, total = rows * d * (s < S ? S : 1);
+          uint8_t* to = dyn + (size_t)stage * row_bytes;
+          Row::last_elements(to, array, at, d, total);
+          mbar_arrive_expect_tx(&full[stage], Row::bytes(at, d, total));
+          Row::copy(to, array, at, d, total, &full[stage]);
           advance();
         }
     }
@@ -316,14 +357,15 @@ __global__ void __launch_bounds__(VPT == 4 ? 544 : MAX_THREADS) k_combine_stream
     const int c = (tid + i * a.tpr) * V;
     if (c < d) {
       w[i].load(static_cast<const E*>(a.w) + c);
-      if (a.w_next) w_next[i].load(static_cast<const E*>(a.w_next) + c);
+      if (COMBINE && a.w_next) w_next[i].load(static_cast<const E*>(a.w_next) + c);
     }
   }
   // the next row of the ring into x (a wait that ran out is reported, and the
   // results are void)
-  auto take = [&]() {
+  auto take = [&](long long element) {
     mbar_wait(&full[stage], phase, &abort_word);
-    const E* row = reinterpret_cast<const E*>(dyn + (size_t)stage * row_bytes);
+    const E* row =
+        reinterpret_cast<const E*>(dyn + (size_t)stage * row_bytes + Row::shift(element));
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (tid + i * a.tpr) * V;
@@ -335,7 +377,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 544 : MAX_THREADS) k_combine_stream
     advance();
   };
   for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
-    if (a.gate) {
+    if (COMBINE && a.gate) {
       const E* g = static_cast<const E*>(a.gate) + (long long)((int)t / a.gate_group) * d;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
@@ -349,22 +391,41 @@ __global__ void __launch_bounds__(VPT == 4 ? 544 : MAX_THREADS) k_combine_stream
 #pragma unroll
       for (int j = 0; j < V; ++j) v[i][j] = 0.f;
     for (int s = 0; s < S; ++s) {
-      take();
+      take((t * S + s) * d);
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) v[i][j] += x[i].get(j);
     }
+    if (!COMBINE) {
+      take(t * d);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] = x[i].get(j);
+    }
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (tid + i * a.tpr) * V;
-      if (a.y && c < d) store_vec<E, V>(static_cast<E*>(a.y) + t * d + c, v[i]);
+      if (COMBINE && a.y && c < d) store_vec<E, V>(static_cast<E*>(a.y) + t * d + c, v[i]);
 #pragma unroll
       for (int j = 0; j < V; ++j) ss = fmaf(v[i][j], v[i][j], ss);
     }
     const float r = inv_rms(sum(ss), d, a.eps);
-    take();
+    if (!COMBINE) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (tid + i * a.tpr) * V;
+        if (c < d) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[i][j] = v[i][j] * r * w[i].get(j);
+          store_vec<E, V>(static_cast<E*>(a.h) + t * d + c, v[i]);
+        }
+      }
+      continue;
+    }
+    take(t * d);
     ss = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -425,7 +486,7 @@ struct BwdArgs {
 // gate row leave s to the join.  All sums are joined in a fixed order: two runs
 // agree bit for bit.
 //
-// Rows of whole vectors reach the threads through shared memory: each row group
+// Rows reach the threads through shared memory: each row group
 // keeps `stages` rows of its operands in flight with bulk copies, across units,
 // and refills a stage as soon as its threads have the row in registers (behind
 // the barrier of the row's sums).
@@ -434,10 +495,15 @@ struct BwdArgs {
 // about 80 instructions a thread, so a thread takes up to 4 vectors of a row,
 // which it holds as they are stored, and a block of up to 512 threads several
 // rows at a time.  One block on each SM.
+//
+// A gate row for every token needs no units: it comes through the ring as a third
+// operand, its gradient leaves with the row, and s collects gate * upstream * n.
 constexpr int BWD_THREADS = 512;
-template <typename E, int V, int VPT, bool GATE>
+enum GateKind { GATE_NONE = 0, GATE_ROWS = 1, GATE_EACH = 2 };
+template <typename E, int V, int VPT, int GATE_KIND>
 __global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
-  constexpr bool RING = V > 1;
+  using Row = SharedRow<E, V>;
+  constexpr bool GATE = GATE_KIND == GATE_ROWS, EACH = GATE_KIND == GATE_EACH;
   grid_dep_sync();
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ float red[2][2][32];
@@ -447,27 +513,25 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
   const int tid = (int)threadIdx.x % a.tpr;
   const int d = a.d;
   const E* w = static_cast<const E*>(a.w);
-  const uint32_t row_bytes = (uint32_t)d * sizeof(E);
-  constexpr bool ADD = !GATE;               // the residual's gradient joins moe_norm's only
+  const uint32_t row_bytes = Row::room(d);
+  constexpr bool ADD = GATE_KIND == GATE_NONE;   // the residual's gradient joins moe_norm's only
   const bool add = ADD && a.add != nullptr;
-  const int parts = add ? 3 : 2;
+  const int parts = add || EACH ? 3 : 2;
   const uint32_t stage_bytes = parts * row_bytes;
   uint8_t* ring = dyn + (size_t)mine * a.stages * stage_bytes;
   // the row groups' sums [rows_here][d], in the ring's place when it has run dry
   // and behind it with gates; with whole gate rows shared by the block the sum
   // for dw [d] follows
   float* joined = reinterpret_cast<float*>(
-      dyn + (RING && GATE ? (size_t)rows_here * a.stages * stage_bytes : 0));
+      dyn + (GATE ? (size_t)rows_here * a.stages * stage_bytes : 0));
   const bool keep = GATE && a.split == 1;   // dw collected over the units
   float* acc = a.alone ? joined + mine * d : joined + rows_here * d;
-  if (RING) {
-    if (tid == 0)
-      for (int s = 0; s < a.stages; ++s) mbar_init(&full[mine][s], 1);
-    if (threadIdx.x == 0) abort_word = 0;
-    fence_barrier_init();
-    fence_proxy_async_smem();
-    __syncthreads();
-  }
+  if (tid == 0)
+    for (int s = 0; s < a.stages; ++s) mbar_init(&full[mine][s], 1);
+  if (threadIdx.x == 0) abort_word = 0;
+  fence_barrier_init();
+  fence_proxy_async_smem();
+  __syncthreads();
 
   // the rows of this row group, unit after unit
   struct Place {
@@ -498,14 +562,15 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
     uint64_t* bar = &full[mine][into];
     uint8_t* to = ring + (size_t)into * stage_bytes;
     if (++into == a.stages) into = 0;
-    mbar_arrive_expect_tx(bar, stage_bytes);
-    const long long at = ahead.t * d;
-    bulk_load_1d(to, static_cast<const E*>(a.v) + at, row_bytes, bar);
-    bulk_load_1d(to + row_bytes, static_cast<const E*>(a.up) + at, row_bytes, bar);
-    if (add) bulk_load_1d(to + 2 * row_bytes, static_cast<const E*>(a.add) + at, row_bytes, bar);
+    const long long at = ahead.t * d, total = (long long)a.T * d;
+    const E* part[3] = {static_cast<const E*>(a.v), static_cast<const E*>(a.up),
+                        static_cast<const E*>(EACH ? a.gate : a.add)};
+    for (int i = 0; i < parts; ++i) Row::last_elements(to + i * row_bytes, part[i], at, d, total);
+    mbar_arrive_expect_tx(bar, parts * Row::bytes(at, d, total));
+    for (int i = 0; i < parts; ++i) Row::copy(to + i * row_bytes, part[i], at, d, total, bar);
     ahead.t += step;
   };
-  if (RING && tid == 0)
+  if (tid == 0)
     for (int s = 0; s < a.stages; ++s) fetch();
 
   const int lane = lane_id(), nw = a.tpr >> 5, w0 = mine * nw;
@@ -603,19 +668,18 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
       else return wr[i].get(j);
     };
     for (; here.t < here.t1; here.t += step) {
-      const E* at = reinterpret_cast<const E*>(ring + (size_t)stage * stage_bytes);
-      if (RING) {
-        // a wait that ran out is reported, and the row's results are void
-        mbar_wait(&full[mine][stage], phase, &abort_word);
-        if (++stage == a.stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+      const uint8_t* at = ring + (size_t)stage * stage_bytes + Row::shift(here.t * d);
+      // a wait that ran out is reported, and the row's results are void
+      mbar_wait(&full[mine][stage], phase, &abort_word);
+      if (++stage == a.stages) {
+        stage = 0;
+        phase ^= 1u;
       }
-      const E* v_row = RING ? at : static_cast<const E*>(a.v) + here.t * d;
-      const E* up_row = RING ? at + d : static_cast<const E*>(a.up) + here.t * d;
-      const E* add_row = RING ? at + 2 * d : static_cast<const E*>(a.add) + here.t * d;
-      Raw<E, V> v[VPT], up[VPT], more[ADD ? VPT : 1];
+      const E* v_row = reinterpret_cast<const E*>(at);
+      const E* up_row = reinterpret_cast<const E*>(at + row_bytes);
+      const E* more_row = reinterpret_cast<const E*>(at + 2 * row_bytes);
+      // `more`: the residual's gradient, or the token's gate
+      Raw<E, V> v[VPT], up[VPT], more[ADD || EACH ? VPT : 1];
       float ss = 0.f, sc = 0.f;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
@@ -623,32 +687,38 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
         if (c < d) {
           v[i].load(v_row + c);
           up[i].load(up_row + c);
+          if constexpr (EACH) more[i].load(more_row + c);
           if constexpr (ADD) {
-            if (add) more[i].load(add_row + c);
+            if (add) more[i].load(more_row + c);
             else more[i].zero();
           }
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             ss = fmaf(v[i].get(j), v[i].get(j), ss);
-            sc = fmaf(v[i].get(j), up[i].get(j) * weight(i, j), sc);
+            sc = fmaf(v[i].get(j), up[i].get(j) * weight(i, j) * (EACH ? more[i].get(j) : 1.f), sc);
           }
         }
       }
       const float2 q = sum2(ss, sc);
-      if (RING && tid == 0) fetch();      // the stage is in registers
+      if (tid == 0) fetch();      // the stage is in registers
       const float r = inv_rms(q.x, d, a.eps);
       const float m = r * r * (q.y / (float)d);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int c = (tid + i * a.tpr) * V;
         if (c < d) {
-          float o[V];
+          float o[V], dg[V];
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            s[i][j] = fmaf(up[i].get(j), v[i].get(j) * r, s[i][j]);
-            o[j] = r * (up[i].get(j) * weight(i, j) - v[i].get(j) * m);
+            const float un = up[i].get(j) * (v[i].get(j) * r);    // upstream * n
+            const float g = EACH ? more[i].get(j) : 1.f;
+            s[i][j] = fmaf(un, g, s[i][j]);
+            if constexpr (EACH) dg[j] = un * weight(i, j);
+            o[j] = r * (up[i].get(j) * weight(i, j) * g - v[i].get(j) * m);
             if constexpr (ADD) o[j] = fmaf(a.res, more[i].get(j), o[j]);
           }
+          if constexpr (EACH)
+            store_vec<E, V>(static_cast<E*>(a.dgate) + here.t * d + c, dg);
           store_vec<E, V>(static_cast<E*>(a.dv) + here.t * d + c, o);
         }
       }

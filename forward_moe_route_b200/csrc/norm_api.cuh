@@ -58,8 +58,8 @@ NormShape norm_shape(const NormDims& D, bool backward) {
     s.threads = norm::BWD_THREADS / s.tpr * s.tpr;
     return s;
   }
-  if (whole && n <= 128) {
-    s.vpt = n <= 32 ? 1 : n <= 64 ? 2 : 4;
+  if (n <= (whole ? 128 : 256)) {
+    s.vpt = !whole ? 8 : n <= 32 ? 1 : n <= 64 ? 2 : 4;
     s.tpr = 32;
     s.threads = 256;
     return s;
@@ -132,10 +132,13 @@ int64_t norm_joined(const NormDims& D, const NormShape& s, const NormCut& c, boo
   const int64_t keep = gate && c.split == 1 && !c.alone ? 1 : 0;
   return (s.rows_here() + keep) * D.d * 4;
 }
+int64_t norm_room(const NormDims& D, const NormShape& s) {
+  if (s.v > 1) return D.d * (D.bf16 ? 2 : 4);
+  return D.bf16 ? norm::SharedRow<__nv_bfloat16, 1>::room((int)D.d)
+                : norm::SharedRow<float, 1>::room((int)D.d);
+}
 int norm_stages(const NormDims& D, const NormShape& s, int parts, int64_t joined) {
-  if (s.v == 1) return 1;
-  const int64_t room = kNormSmem - joined;
-  const int64_t n = room / (s.rows_here() * parts * D.d * (D.bf16 ? 2 : 4));
+  const int64_t n = (kNormSmem - joined) / (s.rows_here() * parts * norm_room(D, s));
   return (int)(n < kNormRing ? n : kNormRing);
 }
 
@@ -153,29 +156,42 @@ NormLayout norm_layout(const NormDims& D, const NormCut& c, bool wide) {
   return L;
 }
 
-// Streams many tokens' rows through shared memory: vectors of up to 4 a thread,
-// as many blocks on an SM as 1024 threads hold, the shared memory divided among
-// them.  Short rows stay with k_norm_fwd's warps.
+// Streams many tokens' rows through shared memory: up to 4 vectors a thread (8 single
+// elements), as many blocks on an SM as 1024 threads hold, the shared memory divided
+// among them.  Short rows stay with k_norm_fwd's warps, and so does moe_norm with
+// rows of whole vectors, which has nothing to wait for between its two passes.
 constexpr int64_t kStreamRow = 2048;      // bytes of a row
 constexpr int64_t kStreamTokens = 592;
-template <typename E>
-moe_status launch_combine_stream(norm::FwdArgs a, int sms, cudaStream_t st) {
-  const int n = a.d / norm::Elem<E>::VEC;
-  const int vpt = n <= 512 ? 1 : n <= 1024 ? 2 : 4;
+bool norm_streams(const NormDims& D, bool combine) {
+  const bool whole = D.d % D.vec == 0;
+  return D.T >= kStreamTokens && (whole ? combine && D.d * (D.bf16 ? 2 : 4) >= kStreamRow &&
+                                              D.d / D.vec <= 2048
+                                        : D.d > 256 && D.d <= 8 * 992);
+}
+template <typename E, bool COMBINE>
+moe_status launch_norm_stream(norm::FwdArgs a, int sms, cudaStream_t st) {
+  constexpr int VEC = norm::Elem<E>::VEC;
+  const bool whole = a.d % VEC == 0;
+  const int n = whole ? a.d / VEC : a.d;
+  const int vpt = !whole ? 8 : n <= 512 ? 1 : n <= 1024 ? 2 : 4;
   a.tpr = ((n + vpt - 1) / vpt + 31) / 32 * 32;
   const int threads = a.tpr + 32;
-  const int per_sm = 1024 / threads < 1 ? 1 : 1024 / threads > 4 ? 4 : 1024 / threads;
-  const int64_t row = (int64_t)a.d * sizeof(E);
+  const int per_sm = 1024 / threads < 1 ? 1 : 1024 / threads > 8 ? 8 : 1024 / threads;
+  const int64_t row = whole ? (int64_t)a.d * sizeof(E) : norm::SharedRow<E, 1>::room(a.d);
   int stages = (int)(kNormSmem / per_sm / row);
   if (stages > norm::STREAM_STAGES) stages = norm::STREAM_STAGES;
-  auto* k = vpt == 1   ? norm::k_combine_stream<E, 1>
-            : vpt == 2 ? norm::k_combine_stream<E, 2>
-                       : norm::k_combine_stream<E, 4>;
+  auto* k = norm::k_norm_stream<E, 1, 8, COMBINE>;
+  if constexpr (COMBINE) {
+    if (whole)
+      k = vpt == 1   ? norm::k_norm_stream<E, VEC, 1, true>
+          : vpt == 2 ? norm::k_norm_stream<E, VEC, 2, true>
+                     : norm::k_norm_stream<E, VEC, 4, true>;
+  }
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)kNormSmem);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (k_combine_stream)");
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (k_norm_stream)");
   const int64_t blocks = a.T < (int64_t)sms * per_sm ? a.T : (int64_t)sms * per_sm;
-  return launch_chain("k_combine_stream", k, dim3((unsigned)blocks), dim3(threads),
+  return launch_chain("k_norm_stream", k, dim3((unsigned)blocks), dim3(threads),
                       (size_t)stages * row, st, a, stages);
 }
 
@@ -199,25 +215,26 @@ moe_status launch_norm_fwd(const NormShape& s, norm::FwdArgs a, int sms, cudaStr
                       dim3((unsigned)(blocks < most ? blocks : most)), dim3(s.threads), 0, st, a);
 }
 
-template <typename E, bool GATE>
+template <typename E, int GATE_KIND>
 moe_status launch_norm_bwd(const NormDims& D, const NormShape& s, const NormCut& c,
                            norm::BwdArgs a, float* dw, cudaStream_t st) {
   constexpr int VEC = norm::Elem<E>::VEC;
+  constexpr bool GATE = GATE_KIND == norm::GATE_ROWS;
   const bool wide = s.vpt == 0;
   if (a.T > 0) {
     auto* k = s.v == 1 ? (wide ? norm::k_norm_bwd_wide<E, 1, GATE>
-                               : norm::k_norm_bwd<E, 1, 16, GATE>)
+                               : norm::k_norm_bwd<E, 1, 16, GATE_KIND>)
               : wide       ? norm::k_norm_bwd_wide<E, VEC, GATE>
-              : s.vpt == 1 ? norm::k_norm_bwd<E, VEC, 1, GATE>
-              : s.vpt == 2 ? norm::k_norm_bwd<E, VEC, 2, GATE>
-                           : norm::k_norm_bwd<E, VEC, 4, GATE>;
+              : s.vpt == 1 ? norm::k_norm_bwd<E, VEC, 1, GATE_KIND>
+              : s.vpt == 2 ? norm::k_norm_bwd<E, VEC, 2, GATE_KIND>
+                           : norm::k_norm_bwd<E, VEC, 4, GATE_KIND>;
     a.tpr = s.tpr;
     size_t smem = 0;
     if (!wide) {
-      const int parts = a.add ? 3 : 2;
+      const int parts = a.add || GATE_KIND == norm::GATE_EACH ? 3 : 2;
       const size_t joined = (size_t)norm_joined(D, s, c, GATE);
       a.stages = norm_stages(D, s, parts, GATE ? (int64_t)joined : 0);
-      smem = s.v > 1 ? (size_t)s.rows_here() * a.stages * parts * a.d * sizeof(E) : 0;
+      smem = (size_t)s.rows_here() * a.stages * parts * norm_room(D, s);
       smem = GATE ? smem + joined : smem > joined ? smem : joined;
       const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)kNormSmem);
@@ -242,14 +259,33 @@ moe_status launch_norm_bwd(const NormDims& D, const NormShape& s, const NormCut&
                       static_cast<E*>(a.dgate), a.d);
 }
 
+// Shape, cut and workspace of a backward pass.  A gate row for every token is cut
+// like none (the looping kernel has only whole gate rows as units).
+struct NormPlan {
+  NormShape s;
+  NormCut c;
+  NormLayout L;
+  int gate;
+};
+NormPlan norm_plan(const NormDims& D, int64_t gate_group) {
+  NormPlan p;
+  p.s = norm_shape(D, true);
+  p.gate = !gate_group ? norm::GATE_NONE
+           : gate_group == 1 && p.s.vpt ? norm::GATE_EACH : norm::GATE_ROWS;
+  NormDims rows = D;
+  if (p.gate != norm::GATE_ROWS) rows.n_gate = 0;
+  p.c = norm_cut(D, p.gate == norm::GATE_ROWS ? gate_group : 0, p.s);
+  p.L = norm_layout(rows, p.c, p.s.vpt == 0);
+  return p;
+}
+
 moe_status norm_backward(const moe_norm_desc& desc, const NormDims& D, bool with_gate,
                          norm::BwdArgs a, float* dw, void* ws, size_t ws_bytes,
                          cudaStream_t st) {
-  const NormShape s = norm_shape(D, true);
-  const NormCut c = norm_cut(D, with_gate ? desc.gate_group : 0, s);
-  NormDims Dg = D;
-  if (!with_gate) Dg.n_gate = 0;
-  const NormLayout L = norm_layout(Dg, c, s.vpt == 0);
+  const NormPlan p = norm_plan(D, with_gate ? desc.gate_group : 0);
+  const NormShape& s = p.s;
+  const NormCut& c = p.c;
+  const NormLayout& L = p.L;
   if (!ws || ws_bytes < L.total || !aligned16(ws)) return MOE_ERR_WORKSPACE;
   int sms;
   const moe_status rc = device_setup(&sms);
@@ -265,11 +301,15 @@ moe_status norm_backward(const moe_norm_desc& desc, const NormDims& D, bool with
   a.alone = c.alone ? 1 : 0;
   a.eps = desc.eps;
   a.res = desc.res_scale;
+  using norm::GATE_EACH, norm::GATE_NONE, norm::GATE_ROWS;
   if (D.bf16)
-    return with_gate ? launch_norm_bwd<__nv_bfloat16, true>(D, s, c, a, dw, st)
-                     : launch_norm_bwd<__nv_bfloat16, false>(D, s, c, a, dw, st);
-  return with_gate ? launch_norm_bwd<float, true>(D, s, c, a, dw, st)
-                   : launch_norm_bwd<float, false>(D, s, c, a, dw, st);
+    return p.gate == GATE_NONE ? launch_norm_bwd<__nv_bfloat16, GATE_NONE>(D, s, c, a, dw, st)
+           : p.gate == GATE_EACH
+               ? launch_norm_bwd<__nv_bfloat16, GATE_EACH>(D, s, c, a, dw, st)
+               : launch_norm_bwd<__nv_bfloat16, GATE_ROWS>(D, s, c, a, dw, st);
+  return p.gate == GATE_NONE   ? launch_norm_bwd<float, GATE_NONE>(D, s, c, a, dw, st)
+         : p.gate == GATE_EACH ? launch_norm_bwd<float, GATE_EACH>(D, s, c, a, dw, st)
+                               : launch_norm_bwd<float, GATE_ROWS>(D, s, c, a, dw, st);
 }
 
 // a required pointer: present and 16-byte aligned
@@ -293,6 +333,9 @@ moe_status moe_norm(const moe_norm_desc* desc, const void* x, const void* w, voi
   memset(&a, 0, sizeof(a));
   a.u = x; a.w = w; a.h = out;
   a.T = (int)D.T; a.d = (int)D.d; a.S = 1; a.eps = desc->eps;
+  if (norm_streams(D, false))
+    return D.bf16 ? launch_norm_stream<__nv_bfloat16, false>(a, sms, stream)
+                  : launch_norm_stream<float, false>(a, sms, stream);
   const NormShape s = norm_shape(D, false);
   return D.bf16 ? launch_norm_fwd<__nv_bfloat16, false>(s, a, sms, stream)
                 : launch_norm_fwd<float, false>(s, a, sms, stream);
@@ -328,10 +371,9 @@ moe_status moe_combine_norm(const moe_norm_desc* desc, const void* x_residual,
   a.h = h; a.y = y; a.x_next = x_next;
   a.T = (int)D.T; a.d = (int)D.d; a.S = desc->n_slots; a.gate_group = desc->gate_group;
   a.eps = desc->eps; a.res = desc->res_scale;
-  if (D.d % D.vec == 0 && D.d * (D.bf16 ? 2 : 4) >= kStreamRow && D.d / D.vec <= 2048 &&
-      D.T >= kStreamTokens)
-    return D.bf16 ? launch_combine_stream<__nv_bfloat16>(a, sms, stream)
-                  : launch_combine_stream<float>(a, sms, stream);
+  if (norm_streams(D, true))
+    return D.bf16 ? launch_norm_stream<__nv_bfloat16, true>(a, sms, stream)
+                  : launch_norm_stream<float, true>(a, sms, stream);
   const NormShape s = norm_shape(D, false);
   return D.bf16 ? launch_norm_fwd<__nv_bfloat16, true>(s, a, sms, stream)
                 : launch_norm_fwd<float, true>(s, a, sms, stream);
@@ -340,13 +382,8 @@ moe_status moe_combine_norm(const moe_norm_desc* desc, const void* x_residual,
 size_t moe_norm_backward_workspace_size(const moe_norm_desc* desc) {
   NormDims D;
   if (norm_dims(desc, &D) != MOE_OK) return 0;
-  const NormShape s = norm_shape(D, true);
-  NormDims plain = D;
-  plain.n_gate = 0;
-  const size_t without =
-      norm_layout(plain, norm_cut(D, 0, s), s.vpt == 0).total;
-  const size_t with =
-      norm_layout(D, norm_cut(D, desc->gate_group, s), s.vpt == 0).total;
+  const size_t without = norm_plan(D, 0).L.total;
+  const size_t with = norm_plan(D, desc->gate_group).L.total;
   return with > without ? with : without;
 }
 

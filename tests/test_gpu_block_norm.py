@@ -218,9 +218,10 @@ def test_graph_and_side_stream():
         assert torch.equal(a, b)
 
 
-# many tokens: rows of 128 vectors, one, two and four vectors a thread, a last thread without any
+# many tokens: rows of 128 vectors, one, two and four vectors a thread, a last thread without any,
+# rows that begin and end inside a vector
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("d", [1024, 1032, 2056, 5120, 8192])
+@pytest.mark.parametrize("d", [1024, 1032, 2056, 5120, 8192, 257, 1001, 7935])
 @pytest.mark.parametrize("slots,gate_group", [(1, 0), (9, 700), (2, 1)])
 def test_combine_norm_of_many_tokens(d, slots, gate_group, dtype):
     gen = torch.Generator(device="cuda").manual_seed(d + slots)
