@@ -32,8 +32,9 @@ moe_status norm_dims(const moe_norm_desc* s, NormDims* D) {
 // How a row is held.  Rows of whole 16-byte vectors are read in vectors
 // (V = 8 bf16 or 4 fp32), others in single elements; rows that do not fit take
 // the looping kernels (vpt = 0).
-// Forward: a row of up to 128 vectors belongs to one warp, a longer one to a block, with one vector a thread when there are fewer
-// rows than SMs and latency counts, else with two or four.
+// Forward: a row of up to 128 vectors or 256 single elements belongs to one warp,
+// a longer one to a block, with one vector a thread when there are fewer rows than
+// SMs and latency counts, else with two or four.
 // Backward: up to 4 vectors (16 single elements) a thread and as many rows a
 // block as it holds.
 constexpr int64_t NORM_SMS = 148;
