@@ -99,6 +99,18 @@ struct Raw {
       word[3] = x.w;
     }
   }
+  // the V elements from column c of a row of d in shared memory, zeros behind its
+  // end.  Single elements are read without a branch (at the row's last one, which
+  // a select then drops): eight branches a row took most of the instructions.
+  __device__ __forceinline__ void load_column(const E* row, int c, int d) {
+    if constexpr (V == 1) {
+      load(row + min(c, d - 1));
+      word[0] = c < d ? word[0] : 0u;
+    } else {
+      if (c < d) load(row + c);
+      else zero();
+    }
+  }
   __device__ __forceinline__ float get(int j) const {
     if constexpr (sizeof(E) == 4) return __uint_as_float(word[j]);
     else return __uint_as_float((j & 1) ? word[j >> 1] & 0xffff0000u : word[j >> 1] << 16);
@@ -376,9 +388,7 @@ __global__ void __launch_bounds__(V > 1 && VPT == 4 ? 544 : MAX_THREADS)
         reinterpret_cast<const E*>(dyn + (size_t)stage * row_bytes + Row::shift(element));
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (tid + i * a.tpr) * V;
-      if (c < d) x[i].load(row + c);
-      else x[i].zero();
+      x[i].load_column(row, (tid + i * a.tpr) * V, d);
     }
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(&empty[stage]);
