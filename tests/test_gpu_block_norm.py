@@ -225,7 +225,7 @@ def test_graph_and_side_stream():
 @pytest.mark.parametrize("slots,gate_group", [(1, 0), (9, 700), (2, 1)])
 def test_combine_norm_of_many_tokens(d, slots, gate_group, dtype):
     gen = torch.Generator(device="cuda").manual_seed(d + slots)
-    T = 1301 if d < 4000 else 593
+    T = 1301 if d < 4000 else 1185
 
     def draw(*shape, std=1.0, mean=0.0):
         x = torch.randn(*shape, generator=gen, device="cuda") * std + mean
