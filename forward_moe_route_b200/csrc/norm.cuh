@@ -180,12 +180,12 @@ struct SharedRow {
 };
 
 struct FwdArgs {
-  const void* u;         // [T, d]: the input of k_norm; the residual of k_combine_norm
+  const void* u;         // [T, d]: the input of moe_norm; the residual of moe_combine_norm
   const void* slots;     // [T, S, d]
   const void* w;         // [d]
   const void* gate;      // [n_gate, d] or null
   const void* w_next;    // [d] or null
-  void* h;               // [T, d]: x of k_norm
+  void* h;               // [T, d]: the result of moe_norm
   void* y;               // [T, d] or null
   void* x_next;          // [T, d] with w_next
   int T, d, S, gate_group;
@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(MAX_THREADS) k_norm_fwd_wide(const FwdArgs a) 
     const E* gate = COMBINE && a.gate
                         ? static_cast<const E*>(a.gate) + (t / a.gate_group) * d
                         : nullptr;
-    // the unrounded h (k_norm: x) of V columns
+    // the unrounded h (moe_norm: its result) of V columns
     auto output = [&](int c, float r, float (&v)[V]) {
       float x[V];
       input(c, v);
