@@ -352,8 +352,10 @@ moe_status moe_combine_norm(const moe_norm_desc* desc, const void* x_residual,
   NormDims D;
   moe_status rc = norm_dims(desc, &D);
   if (rc != MOE_OK) return rc;
+  // without tokens x_next and the gate have no rows, so their addresses may be null
+  if (D.T == 0)
+    return (x_next && !w_next) || (gate && !desc->gate_group) ? MOE_ERR_INVALID_ARG : MOE_OK;
   if (!w_next != !x_next || !gate != !desc->gate_group) return MOE_ERR_INVALID_ARG;
-  if (D.T == 0) return MOE_OK;
   if (!given(x_residual) || !given(y_slots) || !given(w) || !given(h) || !given_or_null(gate) ||
       !given_or_null(w_next) || !given_or_null(y) || !given_or_null(x_next))
     return MOE_ERR_INVALID_ARG;
@@ -414,7 +416,9 @@ moe_status moe_combine_norm_backward(const moe_norm_desc* desc, const void* y, c
   NormDims D;
   moe_status rc = norm_dims(desc, &D);
   if (rc != MOE_OK) return rc;
-  if (!given(dw) || !gate != !desc->gate_group || !gate != !dgate) return MOE_ERR_INVALID_ARG;
+  // without tokens the gate and its gradient have no rows, so their addresses may be null
+  if (!given(dw) || ((gate || dgate) && !desc->gate_group)) return MOE_ERR_INVALID_ARG;
+  if (D.T > 0 && (!gate != !desc->gate_group || !gate != !dgate)) return MOE_ERR_INVALID_ARG;
   if (D.T > 0 && (!given(y) || !given(w) || !given_or_null(gate) || !given(dh) || !given(dy) ||
                   !given_or_null(dgate) || dy == y || dy == w || dy == gate || dy == dh ||
                   dy == dgate || (gate && dgate == gate)))

@@ -505,7 +505,8 @@ moe_status moe_quantize_fp8_blockwise_t(const void* w_bf16, int32_t rows, int32_
  * Outputs must not overlap the inputs or one another; an output at an input's
  * address is refused.  Any d from 1 to 65536 is accepted; rows of whole
  * 16-byte vectors (d a multiple of 8 in bf16, 4 in fp32) run fastest.  Two
- * runs on the same inputs give the same bits. */
+ * runs on the same inputs give the same bits.  With T = 0 every array of rows,
+ * the gate's and dgate's too, is empty and may be NULL, and dw is zeros. */
 typedef struct moe_norm_desc {
   int32_t T;           /* tokens, >= 0 */
   int32_t d;           /* hidden size, 1..65536 */
