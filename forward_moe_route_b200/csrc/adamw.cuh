@@ -405,7 +405,12 @@ __device__ __forceinline__ void step_chunk(const Args& a, const Coef& c, const E
         m_scale = e.m_scale[(at + SPAN) / BLOCK];
         v_scale = e.v_scale[(at + SPAN) / BLOCK];
       }
-      if (!__syncthreads_and(there)) return;   // the span is in registers
+      if (!__syncthreads_and(there)) {         // the span is in registers
+        const int issued = min(i + STAGES, e.spans);
+        if (threadIdx.x == 0)
+          bulk_drain(full, issued % STAGES, (uint32_t)(issued / STAGES) & 1u, STAGES);
+        return;
+      }
       if (threadIdx.x == 0 && i + STAGES < e.spans) fetch(i + STAGES);
     } else {
       held.load(e, at);

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "ring.h"
 
 namespace moe {
 
@@ -34,6 +35,13 @@ __device__ __forceinline__ void bulk_wait_group_read() {
 }
 __device__ __forceinline__ void bulk_wait_group_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// Wait, each time with the usual limit and whatever other threads gave up on, for
+// the copies of a ring with barriers `full` that are in flight (ring_drain).
+__device__ __forceinline__ void bulk_drain(uint64_t* full, int next, uint32_t parity, int stages) {
+  volatile int no_abort = 0;
+  ring_drain(next, parity, stages, [&](int s, uint32_t p) { mbar_wait(&full[s], p, &no_abort); });
 }
 
 }  // namespace moe

@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(V > 1 && VPT == 4 ? 544 : MAX_THREADS)
           Row::copy(to, array, at, d, total, &full[stage]);
           advance();
         }
+      bulk_drain(full, stage, phase, stages);   // of use when the readers gave up
     }
     return;
   }
@@ -380,10 +381,10 @@ __global__ void __launch_bounds__(V > 1 && VPT == 4 ? 544 : MAX_THREADS)
       if (COMBINE && a.w_next) w_next[i].load(static_cast<const E*>(a.w_next) + c);
     }
   }
-  // the next row of the ring into x (a wait that ran out is reported, and the
-  // results are void)
+  // the next row of the ring into x (a wait that ran out is reported, the results
+  // are void, and the copying warp is left to give up too)
   auto take = [&](long long element) {
-    mbar_wait(&full[stage], phase, &abort_word);
+    const bool there = mbar_wait(&full[stage], phase, &abort_word);
     const E* row =
         reinterpret_cast<const E*>(dyn + (size_t)stage * row_bytes + Row::shift(element));
 #pragma unroll
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(V > 1 && VPT == 4 ? 544 : MAX_THREADS)
       x[i].load_column(row, (tid + i * a.tpr) * V, d);
     }
     __syncwarp();
-    if (lane_id() == 0) mbar_arrive(&empty[stage]);
+    if (lane_id() == 0 && there) mbar_arrive(&empty[stage]);
     advance();
   };
   for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
   if (here.unit < a.units) enter(here);
   // thread 0 of the row group fetches rows ahead
   Place ahead = here;
-  int into = 0;
+  int into = 0;          // below 0 (see the rows' loop) once a wait has run out
   auto fetch = [&]() {
     while (ahead.unit < a.units && ahead.t >= ahead.t1) {
       ahead.unit += unit_step;
@@ -687,8 +688,10 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
     };
     for (; here.t < here.t1; here.t += step) {
       const uint8_t* at = ring + (size_t)stage * stage_bytes + Row::shift(here.t * d);
-      // a wait that ran out is reported, and the row's results are void
-      mbar_wait(&full[mine][stage], phase, &abort_word);
+      // a wait that ran out is reported, the results from this row on are void, and
+      // no more rows are fetched
+      if (!mbar_wait(&full[mine][stage], phase, &abort_word) && into >= 0)
+        into = -1 - 2 * into - (int)ring_parity(into, stage, phase);
       if (++stage == a.stages) {
         stage = 0;
         phase ^= 1u;
@@ -718,7 +721,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
         }
       }
       const float2 q = sum2(ss, sc);
-      if (tid == 0) fetch();      // the stage is in registers
+      if (tid == 0 && into >= 0) fetch();      // the stage is in registers
       const float r = inv_rms(q.x, d, a.eps);
       const float m = r * r * (q.y / (float)d);
 #pragma unroll
@@ -770,6 +773,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_norm_bwd(const BwdArgs a) {
       }
     }
   }
+  if (tid == 0 && into < 0) bulk_drain(full[mine], (-1 - into) >> 1, (-1 - into) & 1, a.stages);
   if (GATE && !keep) return;
   auto write = [&](int c, const float (&x)[Q]) {
     store_vec<float, Q>(a.part_w + (long long)blockIdx.x * d + c, x);
