@@ -416,8 +416,10 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
   const int warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
+  // by ordinary loads, here and below: the kernel that writes the offsets may still
+  // run when this one is launched, and grid_dep_sync makes its writes visible to those
   auto rows_of = [&](int g) {
-    const int r0 = __ldg(a.offsets + g), r1 = __ldg(a.offsets + g + 1);
+    const int r0 = a.offsets[g], r1 = a.offsets[g + 1];
     return group_ok(r0, r1, a.n_rows) ? r1 - r0 : 0;
   };
   if (threadIdx.x == 32) {
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     const int l = tile - t.g * per_group;
     t.ot = l / n_it;
     t.it = l - t.ot * n_it;
-    t.row = __ldg(a.offsets + t.g);
+    t.row = a.offsets[t.g];
     t.rows = rows_of(t.g);
     t.nkb = (t.rows + 63) / 64;
     t.cols = (min(TI, a.d_in - t.it * TI) + 31) & ~31;

@@ -1,4 +1,5 @@
-"""The rings in shared memory, on the CPU: which copies a block waits for before it leaves early."""
+"""Memory order of the operators around the layer, on the CPU: which copies a block waits for before
+it leaves early, and how operands are loaded."""
 import os
 import re
 import subprocess
@@ -76,3 +77,14 @@ def test_every_kernel_with_a_ring_of_bulk_copies_drains_it():
                 found += 1
                 assert "bulk_drain(" in part, f"{name}: {part[:200]}"
     assert found == 3
+
+
+def test_no_non_coherent_loads_behind_a_programmatic_launch():
+    """The kernels of the operators around the layer may be launched while the kernel before them
+    still writes their operands: ld.global.nc, which __ldg makes, is for data that stays as it is
+    for a kernel's whole life."""
+    for name in ("norm.cuh", "grouped.cuh", "grouped_few.cuh", "adamw.cuh"):
+        with open(os.path.join(CSRC, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        assert "grid_dep_sync();" in text, name
+        assert not re.search(r"__ldg\(|ld\.global\.nc|__restrict__", text), name
