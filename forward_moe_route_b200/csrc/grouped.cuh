@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
       const Tile t = locate(tile);
       const int acc = tcount & 1;
       const uint32_t use = (uint32_t)(tcount >> 1);
-      if (!mbar_wait(&tfull[acc], use & 1u, abort_flag)) break;
+      if (!mbar_wait_warp(&tfull[acc], use & 1u, abort_flag)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
       const int f0 = t.ft * TF + (int)rank * 128 + q * 32;
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
       const int s = (it - 1) % S;
       const uint32_t ph = (uses >> s) & 1u;
       uses ^= 1u << s;
-      if (!mbar_wait(&tail[s], ph, abort_flag)) break;
+      if (!mbar_wait_warp(&tail[s], ph, abort_flag)) break;
       const int first = t.rows - (t.nkb - 1) * 64, end = (first + 15) & ~15;
       uint8_t* sa = smem + (size_t)s * STAGE_BYTES;
       // a row is one 128-byte line of each of the four boxes; the swizzle
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
         if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&peer_tail[s]), 0));
         continue;
       }
-      if (!mbar_wait(&peer_tail[s], ph, abort_flag)) break;
+      if (!mbar_wait_warp(&peer_tail[s], ph, abort_flag)) break;
       asm volatile("fence.acq_rel.cluster;" ::: "memory");   // the peer's cleared lines
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[s]);
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
       const int acc = tcount & 1;
       const uint32_t use = (uint32_t)(tcount >> 1);
       ++tcount;
-      if (!mbar_wait(&tfull[acc], use & 1u, abort_flag)) break;
+      if (!mbar_wait_warp(&tfull[acc], use & 1u, abort_flag)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
       const bool any = t.rows > 0;

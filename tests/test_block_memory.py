@@ -88,3 +88,31 @@ def test_no_non_coherent_loads_behind_a_programmatic_launch():
             text = re.sub(r"//[^\n]*", "", f.read())
         assert "grid_dep_sync();" in text, name
         assert not re.search(r"__ldg\(|ld\.global\.nc|__restrict__", text), name
+
+
+def blocks_around(text, at):
+    """The statements whose braces enclose position `at`."""
+    heads, start = [], 0
+    for i, c in enumerate(text[:at]):
+        if c in "{};":
+            if c == "{":
+                heads.append(text[start:i])
+            elif c == "}":
+                heads.pop()
+            start = i + 1
+    return heads
+
+
+def test_a_warp_gives_up_as_a_whole():
+    """A wait that one lane gives up on while another sees its barrier complete would leave the
+    second at the warp's next synchronising instruction for good: a wait whose outcome sends lanes
+    different ways is one elected lane's, or the warp votes."""
+    with open(os.path.join(CSRC, "grouped.cuh")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    one, warp = 0, 0
+    for m in re.finditer(r"if \(!mbar_wait(_warp)?\(", text):
+        elected = any("elect_one()" in h for h in blocks_around(text, m.start()))
+        assert elected != bool(m.group(1)), text[m.start():m.start() + 80]
+        one += elected
+        warp += not elected
+    assert one >= 4 and warp >= 4
