@@ -140,6 +140,14 @@ __device__ __forceinline__ float inverse(float x) {
   return r;
 }
 
+// 1 / x with one Newton step on the approximation (Markstein, as for roots8): the
+// nearest float for every x from 2^-100 to 2^14, compared one by one with __frcp_rn,
+// which the other branch of encode8 takes
+__device__ __forceinline__ float inverse_step(float x) {
+  const float near = inverse(x);
+  return fmaf(fmaf(-x, near, 1.0f), near, near);
+}
+
 // The larger and the smaller magnitude of three; a NaN wins the maximum.
 __device__ __forceinline__ float max_nan(float a, float b, float c) {
   float r;
@@ -183,16 +191,15 @@ __device__ __forceinline__ uint32_t encode(float y, uint32_t r4) {
 // as 0.
 //
 // The common case has most <= 2^14 and all of the eight products at 2^-6 or above.
-// Its inverse is the hardware's approximation and one Newton step, which rounds
-// it.  Scaled by 2^-120 too (an exact factor, as 448 / most is not below 2^-6),
+// Its inverse is the hardware's approximation and one Newton step, which rounds it
+// (inverse_step).  Scaled by 2^-120 too (an exact factor, as 448 / most is not below 2^-6),
 // the product's bits are those of `encode` less 960 << 20 without subtracting
 // them.
 template <bool SIGNED, typename R>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float most, R r4) {
   uint32_t c[8];
   float y[8];
-  const float near = inverse(most);
-  const float inv120 = fmaf(fmaf(-most, near, 1.0f), near, near) * 448.0f * 0x1p-120f;
+  const float inv120 = inverse_step(most) * 448.0f * 0x1p-120f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     y[j] = (SIGNED ? fabsf(x[j]) : x[j]) * inv120;
@@ -230,7 +237,8 @@ __device__ __forceinline__ void decode4(uint32_t codes, float s, float* out) {
 // r + (v - r r) y / 2 with the residual exact in a fused multiply-add, to round
 // to the nearest float (Markstein, "Computation of elementary functions on the
 // IBM RISC System/6000 processor", 1990).  Zeros come out as zeros; values whose
-// residual would be subnormal, infinities and NaN take the general root.
+// residual would be subnormal, infinities and NaN take the general root.  Compared
+// with __fsqrt_rn for every float from 0 up.
 __device__ __forceinline__ float roots8(const float (&v)[8], float (&root)[8]) {
   constexpr float LEAST = 0x1p-100f;
 #pragma unroll
