@@ -928,6 +928,11 @@ def moe_adamw(desc, table: AdamwTable, step, lr=None, stream=None) -> None:
     if table.state_bits != desc.state_bits:
         _refuse("moe_adamw", f"a table of {table.state_bits}-bit states")
     on_device = not isinstance(step, int)
+    # numbers would pass for addresses
+    if on_device and not hasattr(step, "data_ptr"):
+        _refuse("moe_adamw", "step is neither an int nor a CUDA tensor")
+    if lr is not None and not hasattr(lr, "data_ptr"):
+        _refuse("moe_adamw", "lr is not a CUDA tensor")
     if not on_device and not 1 <= step < 2 ** 31:
         _refuse("moe_adamw", f"step {step} is not within 1..2^31 - 1")
     at = _operands("moe_adamw", (("table", table.table, 0, _U8, False),

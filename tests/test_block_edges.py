@@ -43,3 +43,17 @@ def test_no_tokens_do_not_excuse_other_mistakes():
     assert L.moe_combine_norm(o, 16, 32, 48, None, None, 64, None, None, None) == bad
     assert L.moe_combine_norm(o, 16, 32, 48, 80, 96, 64, None, None, None) == bad
     assert L.moe_combine_norm_backward(o, 16, 32, 48, 64, 80, 96, None, 112, 0, None) == bad
+
+
+def test_adamw_takes_the_rate_and_the_step_on_the_device_as_tensors():
+    """A number for lr would be read as an address, 0 as no rate at all."""
+    table = moe.AdamwTable(None, 0, 0, 32, [])
+    desc = moe.make_adamw_desc(1e-3)
+    for lr in (0, 0.0, 1e-3, 16):
+        with pytest.raises(moe.MoeError, match="lr") as e:
+            moe.moe_adamw(desc, table, 1, lr=lr)
+        assert e.value.status == moe.ERR_INVALID_ARG
+    for step in (2.0, None, "3"):
+        with pytest.raises(moe.MoeError, match="step") as e:
+            moe.moe_adamw(desc, table, step)
+        assert e.value.status == moe.ERR_INVALID_ARG
