@@ -823,6 +823,9 @@ def _grouped(where: str, function, weight, in_rows, out_rows, offsets, order, *m
     """Check the operands of a grouped product, (name, tensor) each and the weights' type names
     last in `weight`, and call it with the operands in `order`."""
     wname, w, kinds = weight
+    for name, t in ((wname, w), in_rows, out_rows):
+        if t is None:
+            _refuse(where, f"{name} is missing")
     if w.dim() != 3:
         _refuse(where, f"{wname} must be [n_groups, d_out, d_in]")
     G, d_out, d_in = w.shape

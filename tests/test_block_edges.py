@@ -57,3 +57,17 @@ def test_adamw_takes_the_rate_and_the_step_on_the_device_as_tensors():
         with pytest.raises(moe.MoeError, match="step") as e:
             moe.moe_adamw(desc, table, step)
         assert e.value.status == moe.ERR_INVALID_ARG
+
+
+def test_grouped_products_name_what_is_missing():
+    import torch
+    bf = dict(dtype=torch.bfloat16)
+    x, w, y = torch.zeros(9, 16, **bf), torch.zeros(2, 24, 16, **bf), torch.zeros(9, 24, **bf)
+    off = torch.zeros(3, dtype=torch.int32)
+    for call, args, names in ((moe.moe_grouped_mm, (x, w, off, y), "x w offsets y"),
+                              (moe.moe_grouped_mm_dx, (y, w, off, x), "dy w offsets dx"),
+                              (moe.moe_grouped_mm_dw, (y, x, off, w), "dy x offsets dw")):
+        for i, name in enumerate(names.split()):
+            with pytest.raises(moe.MoeError, match=f"{name} is missing") as e:
+                call(*args[:i], None, *args[i + 1:])
+            assert e.value.status == moe.ERR_INVALID_ARG
