@@ -856,7 +856,7 @@ def moe_grouped_mm_dw(dy, x, offsets, dw, accumulate: bool = False, stream=None)
     accumulate (fp32 only) added to dw."""
     _grouped("moe_grouped_mm_dw", _lib.moe_grouped_mm_dw, ("dw", dw, ("float32", "bfloat16")),
              ("x", x), ("dy", dy), offsets, ("dy", "x", "offsets", "dw"),
-             int(dw.element_size() == 2), int(accumulate), stream=stream)
+             int(dw is not None and dw.element_size() == 2), int(accumulate), stream=stream)
 
 
 # ---- AdamW over a list of tensors ------------------------------------------------------------
