@@ -18,10 +18,13 @@
 // step and counted by the element's place, so a step gives the same result
 // however it is split.
 //
-// Bytes an element: 26 with fp32 states and bf16 gradients, 16.1 with 8-bit ones.
-// fp32 states are bound by memory (360M elements 1458 us, 6.9 TB/s); with 8-bit
-// ones the arithmetic of decoding, rounding and the generator comes near it (1074
-// us, 5.4 TB/s, the schedulers 74% busy).  A chunk of one tensor's elements is a
+// Bytes an element, with bf16 gradients and the bf16 copy: 28 with fp32 states, 16.1
+// with 8-bit ones.  fp32 states are bound by memory (360M elements 1460 us, 6.9
+// TB/s); with 8-bit ones the arithmetic of decoding, rounding and the generator
+// comes near it (1050 to 1110 us, 5.5 to 5.2 TB/s, 75 instructions an element, the
+// schedulers issuing in 73% of their active cycles).  Step and rate read from device
+// memory cost every block the coefficients before its first load: 1463 instead of
+// 1458 us, and 7.5 instead of 6.4 us on 96 tensors of 20000.  A chunk of one tensor's elements is a
 // block's; a thread takes 8 elements in a row: one 32-byte access for each fp32
 // operand, and the 16 lanes that share a scale find its maximum with four
 // shuffles.  A table in device memory, written once per list, names the tensor of
@@ -360,8 +363,8 @@ struct Held {
 // The chunk of block blockIdx.x, tensor t of the list.  Whole chunks with 8-bit
 // states come through a ring in shared memory, filled with bulk copies: what the
 // threads hold in registers for a span, and for the next, is too little in flight
-// to cover memory's latency beside 70 instructions an element (1146 us instead of
-// 1074 us for 360M elements).
+// to cover memory's latency beside 75 instructions an element (1146 us instead of
+// 1074 us for 360M elements, measured in turn).
 template <bool STATES8, bool WHOLE, int GRAD>
 __device__ __forceinline__ void step_chunk(const Args& a, const Coef& c, const Entry& e, int t,
                                            uint8_t* ring, uint64_t* full, volatile int* abort) {

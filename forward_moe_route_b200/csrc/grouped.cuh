@@ -30,14 +30,14 @@
 // in global memory.
 //
 // Measured (24570 rows in 64 uneven groups, 2048 x 2816, 283 GFLOP): 226 us alone,
-// 300 us in a loop under the power cap; uniform groups run within 5% of cuBLAS's
+// 312 us in a loop under the power cap; uniform groups run within 5% of cuBLAS's
 // batched product of the same sizes, both bound by the tensor cores' power.  The
-// weight gradients of 24571 rows 2048 x 1408 in bf16 take 180 to 206 us: stores
+// weight gradients of 24571 rows 2048 x 1408 in bf16 take 173 to 207 us: stores
 // that share the SM's way to L2 with the operand loads cost a quarter of it (113 us
 // without them, 150 us with them on equal groups), ragged group ends a tenth.
 //
-// Every CTA reads the offsets itself (no preparing launch); a group whose offsets decrease or leave [0, n_rows] is reported and
-// treated as empty.
+// Every CTA reads the offsets itself (no preparing launch); a group whose offsets
+// decrease or leave [0, n_rows] is reported and treated as empty.
 //
 // Warp roles (384 threads): warp 0 TMA
 // producer, warp 1 MMA issuer (leader CTA), warp 2 TMEM allocator, warp 3 tail

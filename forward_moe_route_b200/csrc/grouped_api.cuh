@@ -41,10 +41,17 @@ moe_status grouped_dims(int32_t n_groups, int32_t n_rows, int32_t d_in, int32_t 
   return MOE_OK;
 }
 
-// Products of at most FEW_MAX rows, two a group on average, whose weights are 64 MB
-// at most stream them by k_few_mm (above, the tensor cores' pipeline is as fast or
-// faster: 6 rows in 6 of 64 groups 2048 x 2816, 69 MB, 15.9 and 16.9 us, 16 rows 41
-// and 35 us; 8 rows of one group 4096 x 4096 26 and 16 us).
+// Products of at most FEW_MAX rows, two a group on average, stream their weights by
+// k_few_mm while these are 64 MiB at most, counted with a group for each row.  Measured,
+// k_few_mm and k_grouped_mm, 2048 x 2816, back to back in a graph and (in brackets) one
+// call with the weights out of L2: one row in each of 4 groups 9.5 and 11.9 us (21.6
+// and 20.5), of 5, 55 MiB, 10.5 and 11.6 (22.7 and 22.5), of 6, 66 MiB, 11.1 and 11.9
+// (26.6 and 24.6), of 8 15.2 and 17.2 (32.8 and 32.8), of 12 34 and 27 (45 and 39).  So
+// just above 64 MiB streaming can still win by 7% from L2 and loses as much from memory;
+// well above it loses.  Each group's rows go by two, so rows that share a group read
+// its weights again: 8 rows of one group 4096 x 4096 35 and 16 us, which the size and
+// the average keep out; all 16 rows in one of 64 groups 512 x 512, 12 and 6 us, they
+// cannot, as the offsets are on the device.
 constexpr int64_t kFewBytes = 64 << 20;
 bool grouped_few(const grouped::Args& a) {
   return a.n_rows <= grouped::FEW_MAX && a.n_rows <= 2 * a.n &&

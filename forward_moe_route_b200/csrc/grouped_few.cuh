@@ -4,8 +4,10 @@
 // A warp takes two weight rows at a time, its lanes 8 elements of the contraction
 // each, four such pieces of either row in flight, and multiplies them with one or
 // two of the group's rows in fp32 on the CUDA cores.  Bound by the weights' bytes
-// and, at these sizes, by latency: a row in 4096 x 4096 9.2 us (k_grouped_mm 15.7
-// us), one row of 64 groups 2048 x 2816 5.2 us (11.4 us).
+// and, at these sizes, by latency.  Back to back in a graph, the weights in L2, and
+// (in brackets) k_grouped_mm: a row in 4096 x 4096 6.8 us (15.4), one row of 64
+// groups 2048 x 2816 4.3 us (10.5); single calls with the weights out of L2 18.4 us
+// (20.5) and 10.2 us (16.4).
 #pragma once
 
 #include "common.cuh"

@@ -16,16 +16,23 @@
 // gradient is sum_t upstream * gate * n, the gate's sum over its tokens of
 // upstream * w * n.
 //
-// These kernels are bound by memory: at most 30 operations per element read.
+// With at most 30 operations per element read, memory is the floor.  The end of a
+// block and the backward before the layer come within 15 to 30% of it in batches.
+// Farther off are the norm before the layer, which asks for nothing ahead of the row
+// at hand (16384 x 7168 bf16 137 us, floor 72), and the backward with gate rows
+// (below).
 //   k_norm_fwd     a row held by one warp (up to 4 vectors of 16 bytes a lane) or
 //                  by one block, its sums warp shuffles and one exchange in shared
 //                  memory
 //   k_norm_stream  many tokens: rows through a ring in shared memory, loads in
 //                  flight while a token's sums are taken (16384 tokens x 9 rows of
-//                  7168 bf16 524 us, 5.8 TB/s; k_norm_fwd 554 us)
+//                  7168 bf16 531 us, 5.7 TB/s; k_norm_fwd 554 us)
 //   k_norm_bwd     the same ring for several rows a block (8192 x 5120 bf16 with
-//                  the residual 63 us, 5.3 TB/s; with the loads of a row behind the
-//                  row before it 119 us)
+//                  the residual 64 us, 5.2 TB/s; with the loads of a row behind the
+//                  row before it 119 us.  Gate rows of 1024 tokens are farther off:
+//                  8191 x 2048 bf16 30 us, floor 15, its warps at their row sums and
+//                  the blocks' sums to be joined; 8192 columns with whole gate rows
+//                  leave the ring one stage: 8192 rows 106 us, floor 63)
 //   *_wide         rows beyond a block's registers, in loops over the columns
 #pragma once
 

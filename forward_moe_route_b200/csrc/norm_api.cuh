@@ -160,7 +160,8 @@ NormLayout norm_layout(const NormDims& D, const NormCut& c, bool wide) {
 // Streams many tokens' rows through shared memory: up to 4 vectors a thread (8 single
 // elements), as many blocks on an SM as 1024 threads hold, the shared memory divided
 // among them.  Short rows stay with k_norm_fwd's warps, and so does moe_norm with
-// rows of whole vectors, which has nothing to wait for between its two passes.
+// rows of whole vectors (16384 x 7168 bf16 137 us, floor 72), for which the ring is
+// not built.
 // Measured, stream and warps or blocks: 4000 tokens x 7 rows of 7168 bf16 110 and
 // 148 us, 16000 x 7 x 1024 fp32 115 and 132 us, 16000 x 7 x 512 bf16 (rows of 1 KB)
 // 53 and 42 us, 700 x 7 x 2048 fp32 14.6 and 11.2 us.
