@@ -220,6 +220,22 @@ moe_status device_setup(int* sms) {
                    gemm8::LAUNCH_REGS);
           return MOE_ERR_UNSUPPORTED;
         }
+      // and so do the grouped products
+      const void* split[4] = {
+          reinterpret_cast<const void*>(grouped::k_grouped_mm<false, grouped::TILE_ROWS>),
+          reinterpret_cast<const void*>(grouped::k_grouped_mm<true, grouped::TILE_ROWS>),
+          reinterpret_cast<const void*>(grouped::k_grouped_dw<false>),
+          reinterpret_cast<const void*>(grouped::k_grouped_dw<true>)};
+      for (const void* k : split) {
+        cudaFuncAttributes f;
+        if (cudaFuncGetAttributes(&f, k) != cudaSuccess) return MOE_ERR_CUDA;
+        if (f.numRegs != grouped::LAUNCH_REGS) {
+          snprintf(t_errmsg, sizeof(t_errmsg),
+                   "grouped product compiled with %d registers a thread, expected %d", f.numRegs,
+                   grouped::LAUNCH_REGS);
+          return MOE_ERR_UNSUPPORTED;
+        }
+      }
     }
     if (!g_encode) {
       void* fn = nullptr;

@@ -6,7 +6,8 @@
 //   dx_r = W_g^T dy_r           k_grouped_mm<true>    (contracts over d_out)
 //   dW_g = sum_r dy_r x_r^T     k_grouped_dw          (contracts over the rows)
 //
-// All operands bf16, accumulation fp32 in TMEM over the whole contraction.
+// All operands bf16, accumulation fp32: in TMEM over segments of the contraction, the
+// segments added in registers (see MM_SEGMENT).
 //
 // k_grouped_mm computes D = (weights) x (rows)^T: 256 features on the UMMA M
 // side, up to 256 rows of one group on the N side, so a group of few rows
@@ -29,7 +30,7 @@
 // of 337 us at 16 groups of 1024 rows, 2048 x 7168.)  No row is copied or padded
 // in global memory.
 //
-// Measured (24570 rows in 64 uneven groups, 2048 x 2816, 283 GFLOP): 226 us alone,
+// Measured (24570 rows in 64 uneven groups, 2048 x 2816, 283 GFLOP): 230 us alone,
 // 312 us in a loop under the power cap; uniform groups run within 5% of cuBLAS's
 // batched product of the same sizes, both bound by the tensor cores' power.  The
 // weight gradients of 24571 rows 2048 x 1408 in bf16 take 173 to 207 us: stores
@@ -41,7 +42,8 @@
 //
 // Warp roles (384 threads): warp 0 TMA
 // producer, warp 1 MMA issuer (leader CTA), warp 2 TMEM allocator, warp 3 tail
-// rows (k_grouped_dw), the rest epilogue.  Two accumulators of 256 columns.
+// rows (k_grouped_dw), the rest epilogue.  Two accumulators of 256 columns, taken by
+// one segment after the other.
 // Barriers and bounded waits as in gemm_t.cuh.
 #pragma once
 
@@ -62,6 +64,29 @@ constexpr int ACC_COLS = 256;
 constexpr int TMEM_COLS = 512;
 constexpr uint32_t BAR_BYTES = (4 * STAGES + 6) * 8 + 16;
 constexpr uint32_t TAB_BYTES = (3 * MAX_GROUPS + 1) * 4 + 12;
+
+// The tensor cores add to the accumulator in TMEM by cutting sums off, not rounding
+// them: every step of 16 loses up to a unit of 2^-23 of the running sum, always
+// towards zero, so the error grows with the length (one group of 32768 rows: 3.8e-5 of
+// a random weight gradient, 1.8e-4 of one whose products have one sign).  So TMEM
+// accumulates segments of a contraction only, and the epilogue warps add these up in
+// fp32 registers, rounded to nearest: the same gradients are then 4.9e-7 and 9.0e-7
+// off at any length.  The next segment's products run meanwhile.
+// Stages (of 64) of a segment.  dW, which may be fp32: 512 rows, as 1024 leave twice
+// the error; 256 rows take the epilogue longer to add than the tensor cores to make
+// (32768 rows 4096 x 4096 767 us, 1024 rows 756, 256 rows 903).  Outputs in bf16: 1024,
+// 1e-6, far below their rounding; with 512 a tile's stores do not fit beside the next
+// one's two segments (batch 250 us and 261 us, 64 groups of 384 rows 247 and 258).
+constexpr int MM_SEGMENT = 16;
+constexpr int DW_SEGMENT = 8;
+
+// The first warpgroup gives registers to the two epilogue warpgroups, which hold 128
+// sums a thread: 128 x 72 + 256 x 216 = 384 x 168, what a block of 384 threads with
+// an SM to itself is launched with (the host checks).
+constexpr int LAUNCH_REGS = 168;
+constexpr int CTRL_REGS = 72;
+constexpr int EPI_REGS = 216;
+static_assert(128 * CTRL_REGS + 256 * EPI_REGS == 384 * LAUNCH_REGS, "register split");
 
 // ---- rows on the N side -------------------------------------------------------------
 constexpr int MM_THREADS = 384;
@@ -251,128 +276,192 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     return t;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer (both CTAs)
-    if (elect_one()) {
-      int it = 0;
-      bool ok = true;
-      for (int tile = tile0; tile < total && ok; tile += tstep) {
-        const Tile t = locate(tile);
-        // the CTA's rows in boxes of 128, 64 and 32, no more than they need: a
-        // tile of few rows is bound by its loads
-        const int half = t.cols / 2, load = (half + 31) & ~31;
-        const uint32_t bytes = HALF_STAGE + (uint32_t)load * 128u;
-        const int xrow = t.row + (int)rank * half;
-        const int f = t.ft * TF + (int)rank * 128;
-        for (int kb = 0; kb < num_kb; ++kb, ++it) {
-          const int s = it % S;
-          const uint32_t ph = (uint32_t)(it / S) & 1u;
-          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag)) { ok = false; break; }
-          uint8_t* sw = smem + (size_t)s * SB;
-          const uint32_t fl = mapa(smem_u32(&full[s]), 0);
-          if (leader) mbar_arrive_expect_tx(&full[s], 2 * bytes);
-          const int k = kb * 64;
-          if (W_MN) {
-            tma_load_3d_pair(&tmW, fl, sw, f, k, t.g);
-            tma_load_3d_pair(&tmW, fl, sw + gbwd::MN_BOX_BYTES, f + 64, k, t.g);
-          } else {
-            tma_load_3d_pair(&tmW, fl, sw, k, f, t.g);
-          }
-          uint8_t* sx = sw + HALF_STAGE;
-          if (ROWS == TILE_ROWS && load == 128) {
-            tma_load_2d_pair(&tmX, fl, sx, k, xrow);
-          } else {
-            if (ROWS == TILE_ROWS && (load & 64)) tma_load_2d_pair(&tmX64, fl, sx, k, xrow);
-            if (load & 32)
-              tma_load_2d_pair(&tmX32, fl, sx + (load & 64) * 128, k, xrow + (load & 64));
+  if (warp < 4) {
+    if constexpr (ROWS == TILE_ROWS)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTRL_REGS));
+    if (warp == 0) {
+      // ------------------------------------------------------------------ TMA producer (both CTAs)
+      if (elect_one()) {
+        int it = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < total && ok; tile += tstep) {
+          const Tile t = locate(tile);
+          // the CTA's rows in boxes of 128, 64 and 32, no more than they need: a
+          // tile of few rows is bound by its loads
+          const int half = t.cols / 2, load = (half + 31) & ~31;
+          const uint32_t bytes = HALF_STAGE + (uint32_t)load * 128u;
+          const int xrow = t.row + (int)rank * half;
+          const int f = t.ft * TF + (int)rank * 128;
+          for (int kb = 0; kb < num_kb; ++kb, ++it) {
+            const int s = it % S;
+            const uint32_t ph = (uint32_t)(it / S) & 1u;
+            if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag)) { ok = false; break; }
+            uint8_t* sw = smem + (size_t)s * SB;
+            const uint32_t fl = mapa(smem_u32(&full[s]), 0);
+            if (leader) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+            const int k = kb * 64;
+            if (W_MN) {
+              tma_load_3d_pair(&tmW, fl, sw, f, k, t.g);
+              tma_load_3d_pair(&tmW, fl, sw + gbwd::MN_BOX_BYTES, f + 64, k, t.g);
+            } else {
+              tma_load_3d_pair(&tmW, fl, sw, k, f, t.g);
+            }
+            uint8_t* sx = sw + HALF_STAGE;
+            if (ROWS == TILE_ROWS && load == 128) {
+              tma_load_2d_pair(&tmX, fl, sx, k, xrow);
+            } else {
+              if (ROWS == TILE_ROWS && (load & 64)) tma_load_2d_pair(&tmX64, fl, sx, k, xrow);
+              if (load & 32)
+                tma_load_2d_pair(&tmX32, fl, sx + (load & 64) * 128, k, xrow + (load & 64));
+            }
           }
         }
+        // the copies this CTA issued land before the block may leave (bounded)
+        volatile int no_abort = 0;
+        for (int j = (it - S > 0 ? it - S : 0); j < it; ++j)
+          mbar_wait(&empty[j % S], (uint32_t)(j / S) & 1u, &no_abort);
       }
-      // the copies this CTA issued land before the block may leave (bounded)
-      volatile int no_abort = 0;
-      for (int j = (it - S > 0 ? it - S : 0); j < it; ++j)
-        mbar_wait(&empty[j % S], (uint32_t)(j / S) & 1u, &no_abort);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer (leader)
-    if (leader && elect_one()) {
-      int it = 0, tcount = 0;
-      bool ok = true;
-      for (int tile = tile0; tile < total && ok; tile += tstep, ++tcount) {
-        const Tile t = locate(tile);
-        const uint32_t idesc = umma_idesc(1, TF, t.cols) | (W_MN ? (1u << 15) : 0u);
-        const int acc = tcount & 1;
-        const uint32_t use = (uint32_t)(tcount >> 1);
-        if (!mbar_wait(&tempty[acc], (use & 1u) ^ 1u, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
-        for (int kb = 0; kb < num_kb; ++kb, ++it) {
-          const int s = it % S;
-          const uint32_t ph = (uint32_t)(it / S) & 1u;
-          if (!mbar_wait(&full[s], ph, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t sw = smem_u32(smem + (size_t)s * SB);
-          const uint64_t wd = W_MN ? gbwd::umma_desc_sw128_mn(sw) : umma_desc_sw128(sw);
-          const uint64_t xd = umma_desc_sw128(sw + HALF_STAGE);
-          constexpr uint64_t w_step = W_MN ? (2048 >> 4) : (32 >> 4);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------------ MMA issuer (leader)
+      if (leader && elect_one()) {
+        int it = 0, scount = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < total && ok; tile += tstep) {
+          const Tile t = locate(tile);
+          const uint32_t idesc = umma_idesc(1, TF, t.cols) | (W_MN ? (1u << 15) : 0u);
+          uint32_t d_tmem = 0;
+          int acc = 0;
+          for (int kb = 0; kb < num_kb; ++kb, ++it) {
+            const bool begins = kb % MM_SEGMENT == 0;
+            if (begins) {
+              acc = scount & 1;
+              const uint32_t use = (uint32_t)(scount >> 1);
+              ++scount;
+              if (!mbar_wait(&tempty[acc], (use & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+              tc_fence_after();
+              d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
+            }
+            const int s = it % S;
+            const uint32_t ph = (uint32_t)(it / S) & 1u;
+            if (!mbar_wait(&full[s], ph, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sw = smem_u32(smem + (size_t)s * SB);
+            const uint64_t wd = W_MN ? gbwd::umma_desc_sw128_mn(sw) : umma_desc_sw128(sw);
+            const uint64_t xd = umma_desc_sw128(sw + HALF_STAGE);
+            constexpr uint64_t w_step = W_MN ? (2048 >> 4) : (32 >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_pair<0>(d_tmem, wd + w_step * k, xd + (uint64_t)(2 * k), idesc,
-                         (kb | k) != 0 ? 1u : 0u);
-          const uint32_t e_local = smem_u32(&empty[s]);
-          umma_commit_pair(mapa(e_local, 0));
-          umma_commit_pair(mapa(e_local, 1));
+            for (int k = 0; k < 4; ++k)
+              umma_pair<0>(d_tmem, wd + w_step * k, xd + (uint64_t)(2 * k), idesc,
+                           !begins || k != 0 ? 1u : 0u);
+            const uint32_t e_local = smem_u32(&empty[s]);
+            umma_commit_pair(mapa(e_local, 0));
+            umma_commit_pair(mapa(e_local, 1));
+            if (kb % MM_SEGMENT == MM_SEGMENT - 1 || kb == num_kb - 1) {
+              const uint32_t t_local = smem_u32(&tfull[acc]);
+              umma_commit_pair(mapa(t_local, 0));
+              umma_commit_pair(mapa(t_local, 1));
+            }
+          }
         }
-        if (ok) {
-          const uint32_t t_local = smem_u32(&tfull[acc]);
-          umma_commit_pair(mapa(t_local, 0));
-          umma_commit_pair(mapa(t_local, 1));
-        }
+        umma_commit_pair(mapa(smem_u32(drain), 0));
+        volatile int no_abort = 0;
+        mbar_wait(drain, 0, &no_abort);
       }
-      umma_commit_pair(mapa(smem_u32(drain), 0));
-      volatile int no_abort = 0;
-      mbar_wait(drain, 0, &no_abort);
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp >= 4) {
+  } else {
+    if constexpr (ROWS == TILE_ROWS)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
     // ------------------------------------------------------------------ epilogue (both CTAs)
     // Warp w reads TMEM lanes 32 (w % 4) .. +31 (32 features) and every other
     // chunk of 16 rows; a chunk is transposed in shared memory and stored as
-    // 64 bytes per row.
+    // 64 bytes per row.  Several segments are added up in registers first (the
+    // chunks' loops unrolled); one goes out chunk by chunk as it is read, in a
+    // loop (512 long, 64 groups of 384 rows: 114 us, through the registers 130).
+    constexpr int CHUNKS = ROWS / 32;              // of a warp
     const int ew = warp - 4, q = warp & 3, par = ew >> 2;
     uint8_t* xb = xpose + (size_t)ew * MM_XPOSE;
     const uint32_t tempty_leader0 = mapa(smem_u32(&tempty[0]), 0);
     const uint32_t tempty_leader1 = mapa(smem_u32(&tempty[1]), 0);
-    int tcount = 0;
-    for (int tile = tile0; tile < total; tile += tstep, ++tcount) {
-      const Tile t = locate(tile);
-      const int acc = tcount & 1;
-      const uint32_t use = (uint32_t)(tcount >> 1);
-      if (!mbar_wait_warp(&tfull[acc], use & 1u, abort_flag)) break;
+    const int segments = (num_kb + MM_SEGMENT - 1) / MM_SEGMENT;
+    int scount = 0;
+    uint32_t tb = 0;          // the warp's lanes of the segment's accumulator
+    auto take = [&]() {
+      const int acc = scount & 1;
+      const uint32_t use = (uint32_t)(scount >> 1);
+      const bool there = mbar_wait_warp(&tfull[acc], use & 1u, abort_flag);
       tc_fence_after();
-      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
-      const int f0 = t.ft * TF + (int)rank * 128 + q * 32;
-      for (int c = par; c * 16 < t.rows; c += 2) {
-        float v[16];
-        tmem_ld16(tb + (uint32_t)(16 * c), v);
+      tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+      return there;
+    };
+    auto release = [&]() {
+      const int acc = scount & 1;
+      tc_fence_before();
+      if (leader) mbar_arrive(&tempty[acc]);
+      else mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
+      ++scount;
+    };
+    bool ok = true;
+    for (int tile = tile0; tile < total && ok; tile += tstep) {
+      const Tile t = locate(tile);
+      // rows 8 m + lane / 4 of a chunk, 8 features
+      const int f = t.ft * TF + (int)rank * 128 + q * 32 + (lane & 3) * 8;
+      int left = f < a.feats ? t.rows - 16 * par - (lane >> 2) : 0;
+      __nv_bfloat16* to = a.y + (size_t)(t.row + 16 * par + (lane >> 2)) * a.feats + f;
+      auto store = [&](const float (&v)[16]) {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           reinterpret_cast<__nv_bfloat16*>(xb)[j * 32 + lane] = __float2bfloat16_rn(v[j]);
         __syncwarp();
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          const int pi = lane + 32 * m, j = pi >> 2, pc = pi & 3;
-          const uint4 val = *reinterpret_cast<const uint4*>(xb + j * 64 + pc * 16);
-          const int r = 16 * c + j, f = f0 + pc * 8;
-          if (r < t.rows && f < a.feats)
-            *reinterpret_cast<uint4*>(a.y + (size_t)(t.row + r) * a.feats + f) = val;
+          const uint4 val = *reinterpret_cast<const uint4*>(xb + (lane + 32 * m) * 16);
+          if (left > 8 * m) *reinterpret_cast<uint4*>(to + (size_t)(8 * m) * a.feats) = val;
         }
         __syncwarp();
+        left -= 32;
+        to += (size_t)32 * a.feats;
+      };
+      if (segments == 1) {
+        if (!(ok = take())) break;
+#pragma unroll 1
+        for (int c = par; c * 16 < t.rows; c += 2) {
+          float v[16];
+          tmem_ld16(tb + (uint32_t)(16 * c), v);
+          store(v);
+        }
+        release();
+        continue;
       }
-      tc_fence_before();
-      if (leader) mbar_arrive(&tempty[acc]);
-      else mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
+      float sum[CHUNKS][16];
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
+      for (int seg = 0; seg < segments; ++seg) {
+        if (!(ok = take())) break;
+#pragma unroll
+        for (int i = 0; i < CHUNKS; i += 2) {      // two loads in flight
+          const int c = par + 2 * i;
+          if (c * 16 < t.rows) {
+            uint32_t v[2][16];
+            tmem_ld16_nowait(tb + (uint32_t)(16 * c), v[0]);
+            tmem_ld16_nowait(tb + (uint32_t)(16 * c + 32), v[1]);
+            tmem_wait_ld2(v[0], v[1]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              sum[i][j] += __uint_as_float(v[0][j]);
+              sum[i + 1][j] += __uint_as_float(v[1][j]);
+            }
+          }
+        }
+        release();
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i)
+        if (par * 16 + i * 32 < t.rows) store(sum[i]);
     }
   }
   tc_fence_before();
@@ -478,123 +567,131 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
   // the group's last stage when its rows end inside a 16-row step
   auto is_tail = [&](const Tile& t, int kb) { return kb == t.nkb - 1 && (t.rows & 15) != 0; };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer (both CTAs)
-    if (elect_one()) {
-      int it = 0;
-      bool ok = true;
-      for (int tile = tile0; tile < total && ok; tile += tstep) {
-        const Tile t = locate(tile);
-        if (idle(t)) continue;
-        const int o = t.ot * TO + (int)rank * 128;
-        const int i = t.it * TI + (int)rank * (t.cols / 2);
-        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-          const int s = it % S;
-          const uint32_t ph = (uint32_t)(it / S) & 1u;
-          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag)) { ok = false; break; }
-          uint8_t* sa = smem + (size_t)s * STAGE_BYTES;
-          const int r = t.row + kb * 64;
-          if (is_tail(t, kb)) {
-            mbar_arrive_expect_tx(&tail[s], STAGE_BYTES);
-            tma_load_2d(&tmDy, &tail[s], sa, o, r);
-            tma_load_2d(&tmDy, &tail[s], sa + BOX, o + 64, r);
-            tma_load_2d(&tmX, &tail[s], sa + 2 * BOX, i, r);
-            tma_load_2d(&tmX, &tail[s], sa + 3 * BOX, i + 64, r);
-          } else {
-            const uint32_t fl = mapa(smem_u32(&full[s]), 0);
-            if (leader) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
-            tma_load_2d_pair(&tmDy, fl, sa, o, r);
-            tma_load_2d_pair(&tmDy, fl, sa + BOX, o + 64, r);
-            tma_load_2d_pair(&tmX, fl, sa + 2 * BOX, i, r);
-            tma_load_2d_pair(&tmX, fl, sa + 3 * BOX, i + 64, r);
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTRL_REGS));
+    if (warp == 0) {
+      // ------------------------------------------------------------------ TMA producer (both CTAs)
+      if (elect_one()) {
+        int it = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < total && ok; tile += tstep) {
+          const Tile t = locate(tile);
+          if (idle(t)) continue;
+          const int o = t.ot * TO + (int)rank * 128;
+          const int i = t.it * TI + (int)rank * (t.cols / 2);
+          for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+            const int s = it % S;
+            const uint32_t ph = (uint32_t)(it / S) & 1u;
+            if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag)) { ok = false; break; }
+            uint8_t* sa = smem + (size_t)s * STAGE_BYTES;
+            const int r = t.row + kb * 64;
+            if (is_tail(t, kb)) {
+              mbar_arrive_expect_tx(&tail[s], STAGE_BYTES);
+              tma_load_2d(&tmDy, &tail[s], sa, o, r);
+              tma_load_2d(&tmDy, &tail[s], sa + BOX, o + 64, r);
+              tma_load_2d(&tmX, &tail[s], sa + 2 * BOX, i, r);
+              tma_load_2d(&tmX, &tail[s], sa + 3 * BOX, i + 64, r);
+            } else {
+              const uint32_t fl = mapa(smem_u32(&full[s]), 0);
+              if (leader) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
+              tma_load_2d_pair(&tmDy, fl, sa, o, r);
+              tma_load_2d_pair(&tmDy, fl, sa + BOX, o + 64, r);
+              tma_load_2d_pair(&tmX, fl, sa + 2 * BOX, i, r);
+              tma_load_2d_pair(&tmX, fl, sa + 3 * BOX, i + 64, r);
+            }
           }
         }
+        volatile int no_abort = 0;
+        for (int j = (it - S > 0 ? it - S : 0); j < it; ++j)
+          mbar_wait(&empty[j % S], (uint32_t)(j / S) & 1u, &no_abort);
       }
-      volatile int no_abort = 0;
-      for (int j = (it - S > 0 ? it - S : 0); j < it; ++j)
-        mbar_wait(&empty[j % S], (uint32_t)(j / S) & 1u, &no_abort);
-    }
-    __syncwarp();
-  } else if (warp == 3) {
-    // ------------------------------------------------------------------ tail rows (both CTAs)
-    if (blockIdx.x == 0)
-      for (int g = lane; g < a.n; g += 32)
-        if (!group_ok(a.offsets[g], a.offsets[g + 1], a.n_rows)) set_status(MOE_ERR_DEVICE_CHECK);
-    int it = 0;
-    uint32_t uses = 0;       // parity of the uses of each stage's tail barrier
-    for (int tile = tile0; tile < total; tile += tstep) {
-      const Tile t = locate(tile);
-      if (idle(t)) continue;
-      it += t.nkb;
-      if (t.nkb == 0 || !is_tail(t, t.nkb - 1)) continue;
-      const int s = (it - 1) % S;
-      const uint32_t ph = (uses >> s) & 1u;
-      uses ^= 1u << s;
-      if (!mbar_wait_warp(&tail[s], ph, abort_flag)) break;
-      const int first = t.rows - (t.nkb - 1) * 64, end = (first + 15) & ~15;
-      uint8_t* sa = smem + (size_t)s * STAGE_BYTES;
-      // a row is one 128-byte line of each of the four boxes; the swizzle
-      // moves 16-byte pieces within a line only
-      for (int j = lane; j < (end - first) * 32; j += 32) {
-        const int row = first + (j >> 5), box = (j >> 3) & 3, piece = j & 7;
-        *reinterpret_cast<uint4*>(sa + box * BOX + row * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
-      }
-      fence_proxy_async_smem();
       __syncwarp();
-      if (!leader) {
-        if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&peer_tail[s]), 0));
-        continue;
-      }
-      if (!mbar_wait_warp(&peer_tail[s], ph, abort_flag)) break;
-      asm volatile("fence.acq_rel.cluster;" ::: "memory");   // the peer's cleared lines
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[s]);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer (leader)
-    if (leader && elect_one()) {
-      int it = 0, tcount = 0;
-      bool ok = true;
-      for (int tile = tile0; tile < total && ok; tile += tstep) {
+    } else if (warp == 3) {
+      // ------------------------------------------------------------------ tail rows (both CTAs)
+      if (blockIdx.x == 0)
+        for (int g = lane; g < a.n; g += 32)
+          if (!group_ok(a.offsets[g], a.offsets[g + 1], a.n_rows)) set_status(MOE_ERR_DEVICE_CHECK);
+      int it = 0;
+      uint32_t uses = 0;       // parity of the uses of each stage's tail barrier
+      for (int tile = tile0; tile < total; tile += tstep) {
         const Tile t = locate(tile);
         if (idle(t)) continue;
-        const uint32_t idesc = umma_idesc(1, TO, t.cols) | (1u << 15) | (1u << 16);
-        const int acc = tcount & 1;
-        const uint32_t use = (uint32_t)(tcount >> 1);
-        ++tcount;
-        if (!mbar_wait(&tempty[acc], (use & 1u) ^ 1u, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
-        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-          const int s = it % S;
-          const uint32_t ph = (uint32_t)(it / S) & 1u;
-          if (!mbar_wait(&full[s], ph, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + (size_t)s * STAGE_BYTES);
-          const uint64_t ad = gbwd::umma_desc_sw128_mn(sa);
-          const uint64_t bd = gbwd::umma_desc_sw128_mn(sa + 2 * BOX);
-          const int steps = min(4, (t.rows - kb * 64 + 15) >> 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps)
-              umma_pair<0>(d_tmem, ad + (uint64_t)(128 * k), bd + (uint64_t)(128 * k), idesc,
-                           (kb | k) != 0 ? 1u : 0u);
-          const uint32_t e_local = smem_u32(&empty[s]);
-          umma_commit_pair(mapa(e_local, 0));
-          umma_commit_pair(mapa(e_local, 1));
+        it += t.nkb;
+        if (t.nkb == 0 || !is_tail(t, t.nkb - 1)) continue;
+        const int s = (it - 1) % S;
+        const uint32_t ph = (uses >> s) & 1u;
+        uses ^= 1u << s;
+        if (!mbar_wait_warp(&tail[s], ph, abort_flag)) break;
+        const int first = t.rows - (t.nkb - 1) * 64, end = (first + 15) & ~15;
+        uint8_t* sa = smem + (size_t)s * STAGE_BYTES;
+        // a row is one 128-byte line of each of the four boxes; the swizzle
+        // moves 16-byte pieces within a line only
+        for (int j = lane; j < (end - first) * 32; j += 32) {
+          const int row = first + (j >> 5), box = (j >> 3) & 3, piece = j & 7;
+          *reinterpret_cast<uint4*>(sa + box * BOX + row * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
         }
-        if (ok) {
-          const uint32_t t_local = smem_u32(&tfull[acc]);
-          umma_commit_pair(mapa(t_local, 0));
-          umma_commit_pair(mapa(t_local, 1));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (!leader) {
+          if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&peer_tail[s]), 0));
+          continue;
         }
+        if (!mbar_wait_warp(&peer_tail[s], ph, abort_flag)) break;
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");   // the peer's cleared lines
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
       }
-      umma_commit_pair(mapa(smem_u32(drain), 0));
-      volatile int no_abort = 0;
-      mbar_wait(drain, 0, &no_abort);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------------ MMA issuer (leader)
+      if (leader && elect_one()) {
+        int it = 0, scount = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < total && ok; tile += tstep) {
+          const Tile t = locate(tile);
+          const uint32_t idesc = umma_idesc(1, TO, t.cols) | (1u << 15) | (1u << 16);
+          uint32_t d_tmem = 0;
+          int acc = 0;
+          for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+            const bool begins = kb % DW_SEGMENT == 0;
+            if (begins) {
+              acc = scount & 1;
+              const uint32_t use = (uint32_t)(scount >> 1);
+              ++scount;
+              if (!mbar_wait(&tempty[acc], (use & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+              tc_fence_after();
+              d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
+            }
+            const int s = it % S;
+            const uint32_t ph = (uint32_t)(it / S) & 1u;
+            if (!mbar_wait(&full[s], ph, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + (size_t)s * STAGE_BYTES);
+            const uint64_t ad = gbwd::umma_desc_sw128_mn(sa);
+            const uint64_t bd = gbwd::umma_desc_sw128_mn(sa + 2 * BOX);
+            const int steps = min(4, (t.rows - kb * 64 + 15) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < steps)
+                umma_pair<0>(d_tmem, ad + (uint64_t)(128 * k), bd + (uint64_t)(128 * k), idesc,
+                             !begins || k != 0 ? 1u : 0u);
+            const uint32_t e_local = smem_u32(&empty[s]);
+            umma_commit_pair(mapa(e_local, 0));
+            umma_commit_pair(mapa(e_local, 1));
+            if (kb % DW_SEGMENT == DW_SEGMENT - 1 || kb == t.nkb - 1) {
+              const uint32_t t_local = smem_u32(&tfull[acc]);
+              umma_commit_pair(mapa(t_local, 0));
+              umma_commit_pair(mapa(t_local, 1));
+            }
+          }
+        }
+        umma_commit_pair(mapa(smem_u32(drain), 0));
+        volatile int no_abort = 0;
+        mbar_wait(drain, 0, &no_abort);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp >= 4) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
     // ------------------------------------------------------------------ epilogue (both CTAs)
     // Blocks of 32 rows x 128 bytes through shared memory to TMA stores (or,
     // accumulating, TMA additions: each element of dW is added to once), which
@@ -603,61 +700,75 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     const int ew = warp - 4, q = warp & 3, par = ew >> 2;
     const uint32_t tempty_leader0 = mapa(smem_u32(&tempty[0]), 0);
     const uint32_t tempty_leader1 = mapa(smem_u32(&tempty[1]), 0);
-    int tcount = 0;
-    for (int tile = tile0; tile < total; tile += tstep) {
+    constexpr int W = OUT_BF16 ? 64 : 32;                   // columns of a block
+    constexpr int BLOCKS = TI / W / 2;                      // of a warp
+    int scount = 0;
+    bool ok = true;
+    for (int tile = tile0; tile < total && ok; tile += tstep) {
       const Tile t = locate(tile);
       if (idle(t)) continue;
-      const int acc = tcount & 1;
-      const uint32_t use = (uint32_t)(tcount >> 1);
-      ++tcount;
-      if (!mbar_wait_warp(&tfull[acc], use & 1u, abort_flag)) break;
-      tc_fence_after();
-      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
-      const bool any = t.rows > 0;
       const int o = t.ot * TO + (int)rank * 128 + q * 32;   // the warp's first output feature
-      constexpr int W = OUT_BF16 ? 64 : 32;                 // columns of a block
       const int chunks = o < a.d_out ? (t.cols + W - 1) / W : 0;
-      for (int c = par; c < chunks; c += 2) {
-        uint8_t* buf = store_buf + (size_t)ew * DW_STAGING;
-        // the last store has read the block
-        if (lane == 0) bulk_wait_group_read<0>();
-        __syncwarp();
+      float sum[BLOCKS][W];                                 // of row `lane`
 #pragma unroll
-        for (int h = 0; h < W / 32; ++h) {
-          uint32_t v[2][16];
-          tmem_ld16_nowait(tb + (uint32_t)(W * c + 32 * h), v[0]);
-          tmem_ld16_nowait(tb + (uint32_t)(W * c + 32 * h + 16), v[1]);
-          tmem_wait_ld2(v[0], v[1]);
-          // row `lane`, 16-byte piece j at j ^ (row % 8) (128-byte swizzle)
+      for (int b = 0; b < BLOCKS; ++b)
 #pragma unroll
-          for (int j = 0; j < (OUT_BF16 ? 4 : 8); ++j) {
-            uint32_t w4[4];
+        for (int j = 0; j < W; ++j) sum[b][j] = 0.f;
+      for (int k0 = 0; k0 < t.nkb; k0 += DW_SEGMENT, ++scount) {
+        const int acc = scount & 1;
+        const uint32_t use = (uint32_t)(scount >> 1);
+        if (!mbar_wait_warp(&tfull[acc], use & 1u, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (OUT_BF16) {
-                const int k = 8 * j + 2 * i;
-                w4[i] = gemm::pack_bf16x2(__uint_as_float(v[k >> 4][k & 15]),
-                                          __uint_as_float(v[k >> 4][(k & 15) + 1]));
-              } else {
-                w4[i] = v[j >> 2][4 * (j & 3) + i];
-              }
-              if (!any) w4[i] = 0u;
+        for (int b = 0; b < BLOCKS; ++b) {
+          const int c = par + 2 * b;
+          if (c < chunks) {
+#pragma unroll
+            for (int h = 0; h < W; h += 32) {
+              uint32_t v[2][16];
+              tmem_ld16_nowait(tb + (uint32_t)(W * c + h), v[0]);
+              tmem_ld16_nowait(tb + (uint32_t)(W * c + h + 16), v[1]);
+              tmem_wait_ld2(v[0], v[1]);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum[b][h + j] += __uint_as_float(v[j >> 4][j & 15]);
             }
-            *reinterpret_cast<uint4*>(buf + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4)) =
-                make_uint4(w4[0], w4[1], w4[2], w4[3]);
           }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (a.accumulate) tma_add_3d(&tmC, buf, t.it * TI + W * c, o, t.g);
-          else gbwd::tma_store_3d(&tmC, buf, t.it * TI + W * c, o, t.g);
-          bulk_commit_group();
+        tc_fence_before();
+        if (leader) mbar_arrive(&tempty[acc]);
+        else mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int b = 0; b < BLOCKS; ++b) {
+        const int c = par + 2 * b;
+        if (c < chunks) {
+          uint8_t* buf = store_buf + (size_t)ew * DW_STAGING;
+          // the last store has read the block
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+          // row `lane`, 16-byte piece j at j ^ (row % 8) (128-byte swizzle)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t w4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w4[i] = OUT_BF16 ? gemm::pack_bf16x2(sum[b][(8 * j + 2 * i) % W],
+                                                   sum[b][(8 * j + 2 * i + 1) % W])
+                               : __float_as_uint(sum[b][(4 * j + i) % W]);
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (a.accumulate) tma_add_3d(&tmC, buf, t.it * TI + W * c, o, t.g);
+            else gbwd::tma_store_3d(&tmC, buf, t.it * TI + W * c, o, t.g);
+            bulk_commit_group();
+          }
         }
       }
-      tc_fence_before();
-      if (leader) mbar_arrive(&tempty[acc]);
-      else mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
     }
     if (lane == 0) bulk_wait_group_all();
     __syncwarp();

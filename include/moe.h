@@ -560,7 +560,8 @@ moe_status moe_combine_norm_backward(const moe_norm_desc* desc, const void* y, c
  *   moe_grouped_mm     y_r  = W_g x_r
  *   moe_grouped_mm_dx  dx_r = W_g^T dy_r
  *   moe_grouped_mm_dw  dW_g = sum_r dy_r x_r^T
- * bf16 operands, fp32 accumulation, each output rounded once.
+ * bf16 operands, fp32 accumulation whose error does not grow with the length of
+ * the contraction, each output rounded once.
  *   x, dx [n_rows, d_in], y, dy [n_rows, d_out], w [n_groups, d_out, d_in] bf16
  *   offsets [n_groups + 1] int32, non-decreasing, within [0, n_rows]; a group
  *     that breaks this counts as empty and sets MOE_ERR_DEVICE_CHECK

@@ -110,7 +110,7 @@ def test_a_warp_gives_up_as_a_whole():
     with open(os.path.join(CSRC, "grouped.cuh")) as f:
         text = re.sub(r"//[^\n]*", "", f.read())
     one, warp = 0, 0
-    for m in re.finditer(r"if \(!mbar_wait(_warp)?\(", text):
+    for m in re.finditer(r"(?:!|= ?)mbar_wait(_warp)?\(", text):
         elected = any("elect_one()" in h for h in blocks_around(text, m.start()))
         assert elected != bool(m.group(1)), text[m.start():m.start() + 80]
         one += elected
